@@ -21,6 +21,12 @@ Entry points (same names as the C functions):
                                          sfq_fmt="ue8m0", sf_zero=1.0, sfb_gran=None)
                                          -> (Q, SFQ)
 
+The operators around the grouped products (routing with its balance loss, the norms around a
+block, orthogonalised expert updates; include/mgg/layer_ops.h) are bound in layer_ops.py and
+exported here too:
+    route_topk, route_topk_backward, block_norm, block_norm_backward, block_residual_norm,
+    block_residual_norm_backward, grouped_newton_schulz
+
 Element types: bfloat16 tensors select BF16; uint8 (or float8_e4m3fn) tensors select
 FP8 E4M3; FP8 activations with weights of K/2 bytes per row (uint8 or float4_e2m1fn_x2)
 select FP8 x FP4 (E2M1 weights, two per byte, 1x32 UE8M0 weight scales "block32").
@@ -41,6 +47,13 @@ __all__ = [
     "quantize_fp8_1x128",
     "swiglu_quant_fp8_1x128",
     "grouped_gemm_contiguous_swiglu_quant",
+    "route_topk",
+    "route_topk_backward",
+    "block_norm",
+    "block_norm_backward",
+    "block_residual_norm",
+    "block_residual_norm_backward",
+    "grouped_newton_schulz",
     "library_path",
     "load_library",
     "MggError",
@@ -95,6 +108,7 @@ def load_library() -> ctypes.CDLL:
               lib.grouped_gemm_kgrouped_psum, lib.quantize_fp8_1x128,
               lib.swiglu_quant_fp8_1x128, lib.grouped_gemm_contiguous_swiglu_quant):
         f.restype = ctypes.c_int
+    layer_ops.declare(lib)
     lib.mgg_status_string.argtypes = [ctypes.c_int]
     lib.mgg_status_string.restype = ctypes.c_char_p
     lib.mgg_last_error.argtypes = []
@@ -376,3 +390,15 @@ def _quant(swiglu, X, Q, SF, sf_fmt, sf_zero):
     with torch.cuda.device(X.device):
         _check(fn(M, K, _ptr(X), _ptr(Q), _ptr(SF), fmt, float(sf_zero), _stream(X.device)))
     return Q, SF
+
+
+from . import layer_ops  # noqa: E402  (it uses the helpers above)
+from .layer_ops import (  # noqa: E402
+    block_norm,
+    block_norm_backward,
+    block_residual_norm,
+    block_residual_norm_backward,
+    grouped_newton_schulz,
+    route_topk,
+    route_topk_backward,
+)

@@ -11,12 +11,16 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB_NAME = "libmoe_grouped_gemm_nt.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ["csrc/grouped_gemm.hip", "csrc/quantize.hip"]
+# csrc/library.hip compiles csrc/grouped_gemm.hip
+SOURCES = ["csrc/library.hip", "csrc/quantize.hip", "csrc/route.hip", "csrc/block_norm.hip",
+           "csrc/newton_schulz.hip"]
 ARCH = "gfx950"
 
 
@@ -43,17 +47,27 @@ def compile_flags(extra=()):
     ]
 
 
-def build(verbose: bool = True, extra=()) -> str:
-    """Compile the library in place; returns its path. Always recompiles."""
-    srcs = [os.path.join(PKG, s) for s in SOURCES]
-    tmp = LIB_PATH + ".tmp"
-    cmd = [hipcc(), *compile_flags(extra), *srcs, "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print("[build]", " ".join(cmd), flush=True)
     res = subprocess.run(cmd, cwd=PKG, capture_output=True, text=True)
     if res.returncode != 0:
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError(f"hipcc failed with exit code {res.returncode}")
+
+
+def build(verbose: bool = True, extra=()) -> str:
+    """Compile the library in place, its sources side by side; returns its path. Always
+    recompiles."""
+    flags = compile_flags(extra)
+    tmp = LIB_PATH + ".tmp"
+    with tempfile.TemporaryDirectory() as objs:
+        jobs = [(os.path.join(PKG, s), os.path.join(objs, os.path.basename(s) + ".o"))
+                for s in SOURCES]
+        obj_flags = [f for f in flags if f != "-shared"] + ["-c"]
+        with ThreadPoolExecutor(max_workers=len(jobs)) as pool:
+            list(pool.map(lambda j: _run([hipcc(), *obj_flags, j[0], "-o", j[1]], verbose), jobs))
+        _run([hipcc(), *flags, *(o for _, o in jobs), "-o", tmp], verbose)
     os.replace(tmp, LIB_PATH)
     if verbose:
         print("[build] wrote", LIB_PATH, flush=True)

@@ -31,6 +31,9 @@ Parity status of each function (what pins it lives in tests/test_oracle_*.py):
       (the format's value table, literal nibble cases, exact-rational brute force over
       raw bytes, one-hot weights, equality with the FP8 channel-scale product when the
       four block scales of each 128-K group agree)
+  layer_ops (routing and its balance loss, the norms around a block, Newton-Schulz updates)
+      pinned (torch's float64 softmax, sigmoid, topk and autograd, finite differences,
+      closed forms; tests/test_oracle_layer_ops.py)
 """
 
 from .formats import (  # noqa: F401
@@ -58,6 +61,7 @@ from .swiglu import (  # noqa: F401
     swiglu_values,
     swiglu_values_exact,
 )
+from . import layer_ops  # noqa: F401
 from .grouped_gemm import (  # noqa: F401
     MX_BLOCK,
     SCALE_K,
