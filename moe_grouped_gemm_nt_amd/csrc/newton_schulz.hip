@@ -27,23 +27,45 @@ typedef _Float16 v4h __attribute__((ext_vector_type(4)));
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
-constexpr int kTile = 128;   // rows and columns of an output tile; operands are padded to it
-constexpr int kSlice = 32;   // K elements staged at once
+constexpr int kSlice = 16;   // K elements of a slice (32 bytes of a row): one MFMA's
 constexpr int kMaxSide = 32768, kMaxMatrices = 4096, kMaxSteps = 32;
-constexpr int kNormBlocks = 64;  // partial sums of squares per matrix
+constexpr int kNormBlocks = 256;  // most partial sums of squares per matrix
 constexpr float kScaleX = 4096.f, kScaleA = 4096.f, kScaleP = 1024.f;
 
-// A matrix as its two fp16 halves, each [rows][ld], `group` elements from one matrix to the
-// next.
+// A matrix [rows][K] as its two fp16 halves, `group` elements from one matrix to the next. Each
+// half is stored slice by slice, [K / 16][rows][16]: a tile's slice is one contiguous run, which
+// spreads over all memory channels whatever K is (rows a power of two apart would meet in one
+// of them), and 32 x 32 results are stored as runs of 1 KB. The two 16-byte pieces of a row
+// change places every eight rows, the order in which LDS holds them: the 16 lanes that a
+// 16-byte LDS read serves at once (0-3, 12-15, 20-23, 24-27 and the other four fours) then
+// meet 64 different banks.
 struct Split {
   _Float16 *hi, *lo;
-  int ld;
+  int rows;
   size_t group;
+  __device__ __forceinline__ size_t at(size_t g, int row, int k) const {
+    return g * group + ((size_t)(k / kSlice) * rows + row) * kSlice +
+           ((k / 8 & 1) ^ (row >> 3 & 1)) * 8 + k % 8;
+  }
 };
 
 __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
+}
+
+// Copies 1 KB, 16 bytes a lane (lane_bytes = 16 * lane), from memory to LDS; both addresses are
+// the wave's. The bytes are there after a wait for the copy and a barrier.
+__device__ __forceinline__ void copy_to_lds(const void* from, void* lds, uint32_t lane_bytes) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)lds);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :: "s"(at), "v"(lane_bytes), "s"(from) : "memory");
+}
+// Waits until at most N of the wave's copies are under way.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" :: "n"(N) : "memory");
 }
 
 struct NsArgs {
@@ -53,19 +75,27 @@ struct NsArgs {
   int M, N;        // as the caller's
   int tall;        // M > N: rows of X are the caller's columns
   float eps, scale;
-  double* norms;   // [G][kNormBlocks]
+  double* norms;   // [G][kNormBlocks], the first norm_blocks of each
+  int norm_blocks;
 };
 
+// Sums of squares in float64: a float32 overflows above 1e19.
 __global__ __launch_bounds__(kThreads) void ns_norm(NsArgs a) {
   __shared__ double s_sum[kThreads / 64];
   const size_t size = (size_t)a.M * a.N, base = size * blockIdx.y;
-  const size_t per = (size + kNormBlocks - 1) / kNormBlocks;
-  const size_t lo = per * blockIdx.x, hi = min(lo + per, size);
   double sum = 0.0;
-  for (size_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-    const float v = a.in_bf16 ? to_f32(reinterpret_cast<const bf16_t*>(a.in)[base + i])
-                              : reinterpret_cast<const float*>(a.in)[base + i];
-    sum += (double)v * (double)v;
+  constexpr int AT_ONCE = 16;
+  for (size_t i0 = (size_t)blockIdx.x * kThreads * AT_ONCE; i0 < size;
+       i0 += (size_t)gridDim.x * kThreads * AT_ONCE) {
+    float v[AT_ONCE];
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) {
+      const size_t i = i0 + u * kThreads + threadIdx.x;
+      v[u] = i >= size ? 0.f : a.in_bf16 ? to_f32(reinterpret_cast<const bf16_t*>(a.in)[base + i])
+                                         : reinterpret_cast<const float*>(a.in)[base + i];
+    }
+#pragma unroll
+    for (int u = 0; u < AT_ONCE; ++u) sum += (double)v[u] * (double)v[u];
   }
   sum = lanes_sum<64>(sum);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
@@ -81,8 +111,11 @@ constexpr int kSplitTile = 64;
 // Scales a matrix to norm 1 and writes X and X^T in halves, padded with zeros.
 __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt) {
   __shared__ float s_tile[kSplitTile][kSplitTile + 1];
+  // every wave adds the partial sums in the same order
   double sum = 0.0;
-  for (int i = 0; i < kNormBlocks; ++i) sum += a.norms[(size_t)blockIdx.z * kNormBlocks + i];
+  for (int i = threadIdx.x & 63; i < a.norm_blocks; i += 64)
+    sum += a.norms[(size_t)blockIdx.z * kNormBlocks + i];
+  sum = lanes_sum<64>(sum);
   const double inv = (double)kScaleX / (sqrt(sum) + (double)a.eps);
   // the caller's rows run along tile rows here
   const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
@@ -102,7 +135,7 @@ __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt
     s_tile[r][col] = v;
     _Float16 hi, lo;
     split(v, hi, lo);
-    const size_t to = blockIdx.z * direct.group + (size_t)i * direct.ld + j;
+    const size_t to = direct.at(blockIdx.z, i, j);
     direct.hi[to] = hi;
     direct.lo[to] = lo;
   }
@@ -110,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt
   for (int r = row; r < kSplitTile; r += kThreads / kSplitTile) {
     _Float16 hi, lo;
     split(s_tile[col][r], hi, lo);
-    const size_t to = blockIdx.z * turned.group + (size_t)(c0 + r) * turned.ld + r0 + col;
+    const size_t to = turned.at(blockIdx.z, c0 + r, r0 + col);
     turned.hi[to] = hi;
     turned.lo[to] = lo;
   }
@@ -121,7 +154,8 @@ enum Product { kGram, kPoly, kApply, kLast };
 struct ProductArgs {
   Split left, right;  // both [rows][K]: C = left right^T
   int K;
-  int tiles_i, tiles_j;
+  int tiles_i, tiles_j;  // of one matrix
+  int whole;             // tiles of all matrices that are not cut into quarters
   float to_value;     // accumulator -> value: the operands' powers of two taken back
   Split c, ct;        // the result and its transpose (symmetric results: the same matrix)
   // kPoly: P = ca I + cb A + cc A A
@@ -130,18 +164,289 @@ struct ProductArgs {
   NsArgs ns;          // kLast
 };
 
-// C = left right^T for one 128 x 128 tile: four waves of 64 x 64 in 32 x 32 x 16 MFMAs, three
-// to a K step (hi hi, hi lo, lo hi). The right operand's rows are the instruction's first
-// operand, so a lane ends up with runs of four consecutive columns of one row of C.
-template <Product WHAT>
-__global__ __launch_bounds__(kThreads) void ns_product(ProductArgs p) {
+// A T x T output tile by WI x WJ waves of (32 RI) x (32 RJ), S slices in LDS.
+template <int T_, int WI_, int WJ_, int S_>
+struct TileOf {
+  static constexpr int T = T_, WI = WI_, WJ = WJ_, S = S_, THREADS = 64 * WI * WJ;
+  static constexpr int RI = T / (32 * WI), RJ = T / (32 * WJ);
+  static constexpr int WAVES = WI * WJ;
+  static constexpr int HALF = T * kSlice * 2;   // bytes of one operand half in a slice
+  static constexpr int STAGE = 4 * HALF;        // left hi, left lo, right hi, right lo
+  static constexpr int COPIES = STAGE / (WAVES * 1024);  // 1 KB copies a wave makes a slice
+  // the epilogue's 32 x 32 words, one row apart by 36: rows and columns both spread over
+  // the banks, rows stay 16-byte aligned
+  static constexpr int TURN_LD = 36, TURN = 32 * TURN_LD * 4;
+  static constexpr int LDS = S * STAGE > WAVES * TURN ? S * STAGE : WAVES * TURN;
+  static_assert(HALF % 1024 == 0, "a copy stays in one operand half");
+  static_assert(S == 4 || S == 8, "the last steps are written out for these");
+};
+
+// Which tile a workgroup takes. Workgroups go to the eight dies in turn, so each die gets a run
+// of consecutive tiles, whose operand rows its L2 then shares.
+__device__ __forceinline__ int tile_of_block(int b, int tiles) {
+  const int per = tiles / 8, whole = per * 8;
+  return b < whole ? (b & 7) * per + (b >> 3) : b;
+}
+
+// LDS accesses of a wave take effect in program order; this keeps the program's order.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ uint32_t pack_halves(float v) {
+  _Float16 hi, lo;
+  split(v, hi, lo);
+  return (uint32_t)__builtin_bit_cast(uint16_t, hi) |
+         (uint32_t)__builtin_bit_cast(uint16_t, lo) << 16;
+}
+
+// Stores the wave's 32 x 32 words at (row, col) of a split matrix.
+__device__ __forceinline__ void store_split(const uint32_t* words, int ld_words, const Split& to,
+                                            size_t g, int row, int col, int lane) {
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = half * 16 + (lane >> 2), c = (lane & 3) * 8;
+    const uint4 a = *reinterpret_cast<const uint4*>(words + r * ld_words + c);
+    const uint4 b = *reinterpret_cast<const uint4*>(words + r * ld_words + c + 4);
+    uint4 hi, lo;
+    hi.x = __builtin_amdgcn_perm(a.y, a.x, 0x05040100);
+    hi.y = __builtin_amdgcn_perm(a.w, a.z, 0x05040100);
+    hi.z = __builtin_amdgcn_perm(b.y, b.x, 0x05040100);
+    hi.w = __builtin_amdgcn_perm(b.w, b.z, 0x05040100);
+    lo.x = __builtin_amdgcn_perm(a.y, a.x, 0x07060302);
+    lo.y = __builtin_amdgcn_perm(a.w, a.z, 0x07060302);
+    lo.z = __builtin_amdgcn_perm(b.y, b.x, 0x07060302);
+    lo.w = __builtin_amdgcn_perm(b.w, b.z, 0x07060302);
+    const size_t at = to.at(g, row + r, col + c);
+    *reinterpret_cast<uint4*>(to.hi + at) = hi;
+    *reinterpret_cast<uint4*>(to.lo + at) = lo;
+  }
+}
+
+// Stores the wave's 32 x 32 floats at (row, col) of the caller's [rows][cols] output.
+__device__ __forceinline__ void store_out(const uint32_t* words, int ld_words, const NsArgs& n,
+                                          size_t g, int row, int col, int lane) {
+  const size_t base = (size_t)n.M * n.N * g;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int r = i * 2 + (lane >> 5), c = lane & 31;
+    if (row + r < n.M && col + c < n.N) {
+      const float v = __uint_as_float(words[r * ld_words + c]);
+      const size_t at = base + (size_t)(row + r) * n.N + col + c;
+      if (n.out_bf16) reinterpret_cast<bf16_t*>(n.out)[at] = from_f32<bf16_t>(v);
+      else reinterpret_cast<float*>(n.out)[at] = v;
+    }
+  }
+}
+
+// C = left right^T for one T x T tile in 32 x 32 x 16 MFMAs, three to a slice of 16 K (hi hi,
+// hi lo, lo hi). The right operand's rows are the instruction's first operand, so a lane ends
+// up with runs of four consecutive columns of one row of C. Slices go straight from memory to
+// a ring of LDS stages; each is read into registers one slice before it is multiplied. Results
+// turn in LDS, so that both C and its transpose are written in 16-byte pieces of their rows.
+//
+// Measured on four 2048 x 2048 matrices: X' takes 175 us, 1180 TFLOP/s of fp16 products (a
+// library product of 8192 x 8192 fp16 matrices reaches 1110 there), with the matrix pipe busy
+// 67 % of the cycles at the 1.7 GHz that the power limit leaves; A and P take 105-115 us.
+template <Product WHAT, class TILE>
+__device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_lds, size_t g,
+                                             int i0, int j0) {
   constexpr bool SYM = WHAT == kGram || WHAT == kPoly;
-  // [operand half: left hi, left lo, right hi, right lo][row][K], the 16-byte pieces of a row
-  // exchanged by its number so that eight consecutive rows meet different banks
-  __shared__ _Float16 s_op[4][kTile][kSlice];
+  constexpr int RI = TILE::RI, RJ = TILE::RJ;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / TILE::WJ * 32 * RI, wj = wave % TILE::WJ * 32 * RJ;
+
+  // copy q of the wave: 1 KB of an operand half's rows, a slice further each time
+  const uint32_t lane_bytes = lane * 16;
+  const uint8_t* from[TILE::COPIES];
+  uint32_t further[TILE::COPIES];
+#pragma unroll
+  for (int q = 0; q < TILE::COPIES; ++q) {
+    const int at = (q * TILE::WAVES + wave) * 1024, h = at / TILE::HALF;
+    const Split& op = h < 2 ? p.left : p.right;
+    const _Float16* half = (h & 1) ? op.lo : op.hi;
+    from[q] = reinterpret_cast<const uint8_t*>(half + g * op.group +
+                                               (size_t)(h < 2 ? i0 : j0) * kSlice) +
+              at % TILE::HALF;
+    further[q] = op.rows * kSlice * 2;
+  }
+  auto copy = [&](int q, int stage) {
+    copy_to_lds(from[q], s_lds + stage * TILE::STAGE + (q * TILE::WAVES + wave) * 1024,
+                lane_bytes);
+    from[q] += further[q];
+  };
+
+  v16f acc[RI][RJ];
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  // a slice of both operands' halves in registers: `left`, `right` hold [half][32 rows]
+  struct Step {
+    v8h left[2][RI], right[2][RJ];
+  };
+  const int at_l = (wi + (lane & 31)) * 32 + ((lane >> 5) ^ (lane >> 3 & 1)) * 16;
+  const int at_r = 2 * TILE::HALF + (wj + (lane & 31)) * 32 +
+                   ((lane >> 5) ^ (lane >> 3 & 1)) * 16;
+  auto read = [&](Step& f, int n, int stage) {  // the n-th of 2 (RI + RJ) reads
+    const uint8_t* base = s_lds + stage * TILE::STAGE;
+    if (n < 2 * RJ)
+      f.right[n / RJ][n % RJ] = *reinterpret_cast<const v8h*>(
+          base + at_r + n / RJ * TILE::HALF + n % RJ * 1024);
+    else
+      f.left[(n - 2 * RJ) / RI][(n - 2 * RJ) % RI] = *reinterpret_cast<const v8h*>(
+          base + at_l + (n - 2 * RJ) / RI * TILE::HALF + (n - 2 * RJ) % RI * 1024);
+  };
+  // One slice: its products, with the reads of the next one (in stage `then`) and the copies of
+  // the one S - 1 further (into stage `into`) spread among them - a wave that issues copies in
+  // a row waits for the copy path, and the matrix pipe with it.
+  auto step = [&](const Step& f, Step& next, int then, int into, bool reads, bool copies) {
+    constexpr int READS = 2 * (RI + RJ);
+#pragma unroll
+    for (int i = 0; i < RI; ++i) {
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.right[0][j], f.left[0][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int n = 0; n < READS; ++n)
+        if (reads && n * RI / READS == i) read(next, n, then);
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.right[1][j], f.left[0][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < TILE::COPIES; ++q)
+        if (copies && q * RI / TILE::COPIES == i) copy(q, into);
+#pragma unroll
+      for (int j = 0; j < RJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f.right[0][j], f.left[1][i], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // At the end of step s the copies of slice s + 2 have landed and everyone has read slice
+  // s + 1, so step s + 1 may read the one and step s + 2 copy over the other. While copies go
+  // on, those of the S - 3 slices behind s + 2 may still be under way.
+  constexpr int S = TILE::S, AHEAD = S - 1;
+  const int slices = p.K / kSlice;  // a multiple of four
+  Step even, odd;
+  for (int s = 0; s < AHEAD && s < slices; ++s)
+#pragma unroll
+    for (int q = 0; q < TILE::COPIES; ++q) copy(q, s);
+  if (slices >= AHEAD) wait_copies<(AHEAD - 2) * TILE::COPIES>();
+  else wait_copies<0>();
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < 2 * (RI + RJ); ++n) read(even, n, 0);
+  // N steps from stage 0 on, of which the last LEFT have no slice left to copy.
+  auto steps = [&](auto count, auto left) {
+    constexpr int N = count(), LEFT = left();
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const bool copies = n < N - LEFT, reads = LEFT == 0 || n + 1 < N;
+      if (n % 2 == 0) step(even, odd, (n + 1) % S, (n + S - 1) % S, reads, copies);
+      else step(odd, even, (n + 1) % S, (n + S - 1) % S, reads, copies);
+      if (copies) wait_copies<(AHEAD - 2) * TILE::COPIES>();
+      else wait_copies<0>();
+      __syncthreads();
+    }
+  };
+  using std::integral_constant;
+  int todo = slices;
+  for (; todo > 2 * S - 2; todo -= S)
+    steps(integral_constant<int, S>{}, integral_constant<int, 0>{});
+  // with S = 4 four slices are left, with S = 8 four, eight or twelve
+  if (S == 4 || todo == 4) {
+    steps(integral_constant<int, 4>{}, integral_constant<int, AHEAD < 4 ? AHEAD : 4>{});
+  } else if (todo == 8) {
+    steps(integral_constant<int, 8>{}, integral_constant<int, AHEAD>{});
+  } else {
+    steps(integral_constant<int, 12>{}, integral_constant<int, AHEAD>{});
+  }
+  // the stages become the waves' turning space
+
+  // lane: row 32 i + (lane & 31) of the wave's part; registers 4 q .. 4 q + 3: columns
+  // 32 j + 8 q + 4 (lane >> 5) ..
+  uint32_t* turn = reinterpret_cast<uint32_t*>(s_lds + wave * TILE::TURN);
+  constexpr int LD = TILE::TURN_LD;
+  const bool mirror = !SYM || i0 != j0;
+#pragma unroll
+  for (int i = 0; i < RI; ++i)
+#pragma unroll
+    for (int j = 0; j < RJ; ++j) {
+      const int row0 = i0 + wi + 32 * i, col0 = j0 + wj + 32 * j;
+      uint32_t w[16];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * p.to_value;
+        if constexpr (WHAT == kPoly) {
+          const int row = row0 + (lane & 31), col = col0 + 8 * q + 4 * (lane >> 5);
+          const size_t at = p.a.at(g, row, col);
+          const v4h hi = *reinterpret_cast<const v4h*>(p.a.hi + at);
+          const v4h lo = *reinterpret_cast<const v4h*>(p.a.lo + at);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float av = ((float)hi[e] + (float)lo[e]) * (1.f / kScaleA);
+            v[e] = fmaf(p.cc, v[e], p.cb * av) + (row == col + e ? p.ca : 0.f);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[4 * q + e] = WHAT == kLast ? __float_as_uint(v[e] * p.ns.scale)
+                                       : pack_halves(v[e] * (WHAT == kGram ? kScaleA
+                                                             : WHAT == kPoly ? kScaleP : kScaleX));
+      }
+      // each lane group reads back what other lanes of its own wave wrote
+      const bool direct = WHAT != kLast || !p.ns.tall;
+      if (direct) {
+        wave_order();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(turn + (lane & 31) * LD + 8 * q + 4 * (lane >> 5)) =
+              make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+        wave_order();
+        if constexpr (WHAT == kLast) store_out(turn, LD, p.ns, g, row0, col0, lane);
+        else store_split(turn, LD, p.c, g, row0, col0, lane);
+      }
+      if (WHAT == kLast ? p.ns.tall : mirror) {
+        wave_order();
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            turn[(8 * q + 4 * (lane >> 5) + e) * LD + (lane & 31)] = w[4 * q + e];
+        wave_order();
+        if constexpr (WHAT == kLast) store_out(turn, LD, p.ns, g, col0, row0, lane);
+        else store_split(turn, LD, p.ct, g, col0, row0, lane);
+      }
+    }
+}
+
+// All tiles of a product: `whole` of them in the tile's own size, the rest, which would be left
+// over for a round of their own on a few CUs, in quarters. The quarter below the diagonal of a
+// symmetric result's diagonal tile is its mirror's.
+template <Product WHAT, class TILE, class QUARTER>
+__global__ __launch_bounds__(TILE::THREADS) void ns_product(ProductArgs p) {
+  constexpr bool SYM = WHAT == kGram || WHAT == kPoly;
+  constexpr int T = TILE::T;
+  extern __shared__ __align__(16) uint8_t s_lds[];
+  int b = blockIdx.x, quarter = -1;
+  if (b < p.whole) {
+    b = tile_of_block(b, p.whole);
+  } else {
+    quarter = (b - p.whole) & 3;
+    b = p.whole + ((b - p.whole) >> 2);
+  }
+  const int per_matrix = SYM ? p.tiles_i * (p.tiles_i + 1) / 2 : p.tiles_i * p.tiles_j;
+  const size_t g = b / per_matrix;
+  b %= per_matrix;
   int ti, tj;
   if constexpr (SYM) {  // the b-th pair i <= j, rows of the triangle one after another
-    int b = blockIdx.x;
     ti = 0;
     for (int len = p.tiles_i; b >= len; --len) {
       b -= len;
@@ -149,131 +454,77 @@ __global__ __launch_bounds__(kThreads) void ns_product(ProductArgs p) {
     }
     tj = ti + b;
   } else {
-    ti = blockIdx.x / p.tiles_j;
-    tj = blockIdx.x % p.tiles_j;
+    ti = b / p.tiles_j;
+    tj = b % p.tiles_j;
   }
-  const int i0 = ti * kTile, j0 = tj * kTile;
-  const size_t g = blockIdx.y;
-  const _Float16* src[4] = {p.left.hi + g * p.left.group + (size_t)i0 * p.left.ld,
-                            p.left.lo + g * p.left.group + (size_t)i0 * p.left.ld,
-                            p.right.hi + g * p.right.group + (size_t)j0 * p.right.ld,
-                            p.right.lo + g * p.right.group + (size_t)j0 * p.right.ld};
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int wi = (wave >> 1) * 64, wj = (wave & 1) * 64;  // the wave's place in the tile
-  v16f acc[2][2];  // [i][j]
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-
-  auto piece = [](int row, int c) { return c ^ ((row >> 1) & 3); };
-  for (int k0 = 0; k0 < p.K; k0 += kSlice) {
-    __syncthreads();
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int ld = h < 2 ? p.left.ld : p.right.ld;
-#pragma unroll
-      for (int q = 0; q < kTile * 4 / kThreads; ++q) {
-        const int at = q * kThreads + threadIdx.x, row = at >> 2, c = at & 3;
-        *reinterpret_cast<v8h*>(&s_op[h][row][piece(row, c) * 8]) =
-            *reinterpret_cast<const v8h*>(src[h] + (size_t)row * ld + k0 + c * 8);
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kSlice / 16; ++kk) {
-      v8h l[2][2], r[2][2];  // [half][32-row part]
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int c = kk * 2 + (lane >> 5);
-          const int li = wi + t * 32 + (lane & 31), ri = wj + t * 32 + (lane & 31);
-          l[h][t] = *reinterpret_cast<const v8h*>(&s_op[h][li][piece(li, c) * 8]);
-          r[h][t] = *reinterpret_cast<const v8h*>(&s_op[2 + h][ri][piece(ri, c) * 8]);
-        }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[0][j], l[0][i], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[1][j], l[0][i], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(r[0][j], l[1][i], acc[i][j], 0, 0, 0);
-        }
-    }
+  if (quarter < 0) {
+    tile_product<WHAT, TILE>(p, s_lds, g, ti * T, tj * T);
+  } else if constexpr (TILE::T != QUARTER::T) {
+    static_assert(TILE::T == 2 * QUARTER::T && TILE::THREADS == QUARTER::THREADS, "a quarter");
+    if (SYM && ti == tj && quarter == 2) return;
+    tile_product<WHAT, QUARTER>(p, s_lds, g, ti * T + (quarter >> 1) * QUARTER::T,
+                                tj * T + (quarter & 1) * QUARTER::T);
   }
+}
 
-  // lane: row i0 + wi + 32 i + (lane & 31); registers 4 q .. 4 q + 3: columns
-  // j0 + wj + 32 j + 8 q + 4 (lane >> 5) ..
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = i0 + wi + 32 * i + (lane & 31);
-        const int col = j0 + wj + 32 * j + 8 * q + 4 * (lane >> 5);
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e] * p.to_value;
-        if constexpr (WHAT == kLast) {
-          const NsArgs& n = p.ns;
-          const int rows = n.tall ? n.N : n.M, cols = n.tall ? n.M : n.N;
-          const size_t base = (size_t)n.M * n.N * g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (row < rows && col + e < cols) {
-              const size_t at = base + (n.tall ? (size_t)(col + e) * n.N + row
-                                               : (size_t)row * n.N + col + e);
-              const float o = v[e] * n.scale;
-              if (n.out_bf16) reinterpret_cast<bf16_t*>(n.out)[at] = from_f32<bf16_t>(o);
-              else reinterpret_cast<float*>(n.out)[at] = o;
-            }
-        } else {
-          float power = WHAT == kGram ? kScaleA : WHAT == kPoly ? kScaleP : kScaleX;
-          if constexpr (WHAT == kPoly) {
-            const size_t at = g * p.a.group + (size_t)row * p.a.ld + col;
-            const v4h hi = *reinterpret_cast<const v4h*>(p.a.hi + at);
-            const v4h lo = *reinterpret_cast<const v4h*>(p.a.lo + at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float av = ((float)hi[e] + (float)lo[e]) * (1.f / kScaleA);
-              v[e] = fmaf(p.cc, v[e], p.cb * av) + (row == col + e ? p.ca : 0.f);
-            }
-          }
-          v4h hi, lo;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            _Float16 h, l;
-            split(v[e] * power, h, l);
-            hi[e] = h;
-            lo[e] = l;
-          }
-          const size_t at = g * p.c.group + (size_t)row * p.c.ld + col;
-          *reinterpret_cast<v4h*>(p.c.hi + at) = hi;
-          *reinterpret_cast<v4h*>(p.c.lo + at) = lo;
-          if (!SYM || ti != tj) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const size_t mirrored = g * p.ct.group + (size_t)(col + e) * p.ct.ld + row;
-              p.ct.hi[mirrored] = hi[e];
-              p.ct.lo[mirrored] = lo[e];
-            }
-          }
-        }
-      }
+using Tile64 = TileOf<64, 2, 2, 8>;
+using Tile128 = TileOf<128, 2, 2, 4>;
+using Tile256 = TileOf<256, 2, 4, 4>;
+using Quarter128 = TileOf<64, 2, 2, 4>;
+using Quarter256 = TileOf<128, 2, 4, 4>;
+
+// How a product is dealt to the 256 CUs, one workgroup of Tile256 or two of the others on each.
+struct Deal {
+  int tile, whole, blocks;  // tile size, tiles kept whole, workgroups
+  double cost;
+};
+
+// Larger tiles copy fewer bytes for each product, smaller ones leave fewer CUs without work.
+// Costs are relative to a full round of Tile256, from measurements with K = 2048: full rounds
+// of 256 x 256, 512 x 128 and 512 x 64 tiles take 175, 98 and 41 us; what is left over takes
+// 61 (128-tiles, one to a CU) or 31 us (64-tiles), or is cut into quarters when those fit one
+// round (0.35 of a Tile256, 0.2 in all for Tile128).
+Deal deal(int tile, long tiles) {
+  const int slots = tile == 256 ? 256 : 512;
+  const long full = tiles / slots, left = tiles % slots;
+  const bool cut = tile > 64 && left > 0 && left <= slots / 4;
+  const double round = tile == 256 ? 1.0 : tile == 128 ? 0.56 : 0.236;
+  const double rest = left == 0 ? 0.0
+                      : tile == 256 ? (cut ? 0.35 : 1.0)
+                      : tile == 128 ? (cut ? 0.2 : left <= 256 ? 0.35 : 0.56)
+                                    : (left <= 256 ? 0.175 : 0.236);
+  const long whole = cut ? tiles - left : tiles;
+  return Deal{tile, (int)whole, (int)(whole + (tiles - whole) * 4), full * round + rest};
+}
+
+// The cheapest deal of G matrices of rows x cols (multiples of 64 at least).
+Deal best_deal(int G, int rows, int cols, bool symmetric) {
+  Deal best{};
+  for (int tile : {256, 128, 64}) {
+    const long ti = cdiv(rows, tile), tj = cdiv(cols, tile);
+    const Deal d = deal(tile, G * (symmetric ? ti * (ti + 1) / 2 : ti * tj));
+    if (tile == 256 || d.cost < best.cost) best = d;
+  }
+  return best;
 }
 
 struct Workspace {
   int m, n, mp, np;
+  Deal symmetric, apply;
   size_t x, xt[2], a, p, norms, bytes;
   Workspace(int G, int M, int N) {
     m = std::min(M, N);
     n = std::max(M, N);
-    mp = cdiv(m, kTile) * kTile;
-    np = cdiv(n, kTile) * kTile;
+    symmetric = best_deal(G, m, m, true);
+    apply = best_deal(G, m, n, false);
+    // both sides in whole tiles of both
+    const int pad = std::max(symmetric.tile, apply.tile);
+    mp = cdiv(m, pad) * pad;
+    np = cdiv(n, pad) * pad;
+    // the tiles of the padded sides
+    const long s = mp / symmetric.tile;
+    symmetric = deal(symmetric.tile, G * (s * (s + 1) / 2));
+    apply = deal(apply.tile, (long)G * (mp / apply.tile) * (np / apply.tile));
     const size_t big = (size_t)G * mp * np * 2 * sizeof(_Float16);
     const size_t small = (size_t)G * mp * mp * 2 * sizeof(_Float16);
     x = 0;
@@ -284,9 +535,9 @@ struct Workspace {
     norms = p + small;
     bytes = round_up(norms + (size_t)G * kNormBlocks * sizeof(double), 256);
   }
-  Split at(void* base, size_t off, int G, int rows, int ld) const {
+  Split at(void* base, size_t off, int G, int rows, int k) const {
     _Float16* hi = reinterpret_cast<_Float16*>((char*)base + off);
-    return Split{hi, hi + (size_t)G * rows * ld, ld, (size_t)rows * ld};
+    return Split{hi, hi + (size_t)G * rows * k, rows, (size_t)rows * k};
   }
 };
 
@@ -355,23 +606,46 @@ mgg_status grouped_newton_schulz(mgg_act dt, mgg_act out_dt, int G, int M, int N
   Split xt = ws.at(workspace, ws.xt[0], G, np, mp), xt_next = ws.at(workspace, ws.xt[1], G, np, mp);
   const Split a = ws.at(workspace, ws.a, G, mp, mp), p = ws.at(workspace, ws.p, G, mp, mp);
   const NsArgs ns{X, out, dt == MGG_ACT_BF16, out_dt == MGG_ACT_BF16, M, N, M > N, eps, scale,
-                  reinterpret_cast<double*>((char*)workspace + ws.norms)};
-  ns_norm<<<dim3(kNormBlocks, G), kThreads, 0, stream>>>(ns);
+                  reinterpret_cast<double*>((char*)workspace + ws.norms),
+                  (int)std::min<long>(kNormBlocks, ((long)M * N + 4095) / 4096)};
+  ns_norm<<<dim3(ns.norm_blocks, G), kThreads, 0, stream>>>(ns);
   const int rows = M > N ? np : mp, cols = M > N ? mp : np;
   ns_split<<<dim3(cols / kSplitTile, rows / kSplitTile, G), kThreads, 0, stream>>>(ns, x, xt);
-  const int tm = mp / kTile, tn = np / kTile;
-  for (int s = 0; s < steps; ++s) {
-    ProductArgs gram{x, x, np, tm, tm, 1.f / (kScaleX * kScaleX), a, a, a, 0.f, 0.f, 0.f, ns};
-    ns_product<kGram><<<dim3(tm * (tm + 1) / 2, G), kThreads, 0, stream>>>(gram);
-    ProductArgs poly{a, a, mp, tm, tm, 1.f / (kScaleA * kScaleA), p, p, a,
-                     coeffs[3 * s], coeffs[3 * s + 1], coeffs[3 * s + 2], ns};
-    ns_product<kPoly><<<dim3(tm * (tm + 1) / 2, G), kThreads, 0, stream>>>(poly);
-    ProductArgs apply{p, xt, mp, tm, tn, 1.f / (kScaleP * kScaleX), x, xt_next, a,
-                      0.f, 0.f, 0.f, ns};
-    if (s + 1 < steps) ns_product<kApply><<<dim3(tm * tn, G), kThreads, 0, stream>>>(apply);
-    else ns_product<kLast><<<dim3(tm * tn, G), kThreads, 0, stream>>>(apply);
+  auto run_tile = [&](auto tile, auto quarter, auto what, const Deal& deal, ProductArgs args) {
+    using TILE = decltype(tile);
+    args.tiles_i = mp / TILE::T;
+    args.tiles_j = (what() == kGram || what() == kPoly ? mp : np) / TILE::T;
+    args.whole = deal.whole;
+    auto kernel = ns_product<what(), TILE, decltype(quarter)>;
+    if (TILE::LDS > 64 * 1024 &&
+        hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize,
+                            TILE::LDS) != hipSuccess)
+      return false;
+    kernel<<<deal.blocks, TILE::THREADS, TILE::LDS, stream>>>(args);
+    return true;
+  };
+  auto run = [&](auto what, const ProductArgs& args) {
+    const Deal& d = what() == kGram || what() == kPoly ? ws.symmetric : ws.apply;
+    return d.tile == 64    ? run_tile(Tile64{}, Tile64{}, what, d, args)
+           : d.tile == 128 ? run_tile(Tile128{}, Quarter128{}, what, d, args)
+                           : run_tile(Tile256{}, Quarter256{}, what, d, args);
+  };
+  bool ok = true;
+  for (int s = 0; s < steps && ok; ++s) {
+    const ProductArgs gram{x, x, np, 0, 0, 0, 1.f / (kScaleX * kScaleX), a, a, a,
+                           0.f, 0.f, 0.f, ns};
+    const ProductArgs poly{a, a, mp, 0, 0, 0, 1.f / (kScaleA * kScaleA), p, p, a,
+                           coeffs[3 * s], coeffs[3 * s + 1], coeffs[3 * s + 2], ns};
+    const ProductArgs apply{p, xt, mp, 0, 0, 0, 1.f / (kScaleP * kScaleX), x, xt_next, a,
+                            0.f, 0.f, 0.f, ns};
+    using std::integral_constant;
+    ok = run(integral_constant<Product, kGram>{}, gram) &&
+         run(integral_constant<Product, kPoly>{}, poly) &&
+         (s + 1 < steps ? run(integral_constant<Product, kApply>{}, apply)
+                        : run(integral_constant<Product, kLast>{}, apply));
     std::swap(xt, xt_next);
   }
+  if (!ok) return fail(MGG_EHIP, "hipFuncSetAttribute failed");
   return launched();
 }
 
