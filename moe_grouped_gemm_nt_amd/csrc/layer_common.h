@@ -31,7 +31,7 @@ inline bool aligned(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
 inline size_t elem_bytes(mgg_act dt) { return dt == MGG_ACT_BF16 ? 2 : 4; }
 inline bool known(mgg_act dt) { return dt == MGG_ACT_BF16 || dt == MGG_ACT_F32; }
 constexpr size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
-constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 struct bf16_t {
   uint16_t bits;
@@ -70,12 +70,51 @@ __device__ __forceinline__ void sigmoid_parts(float v, float& q, float& one_minu
   one_minus_q = v >= 0.f ? a * r : r;
 }
 
-// Sum, or another associative operation, over the L lanes (a power of two up to 64) that
-// share a row; every lane gets the result.
+// op of the lane's own value and its partner's, OFF = 1, 2, 4, 8, 16 or 32 lanes away, for a
+// commutative op. The partner is lane ^ OFF for 1, 2, 16 and 32, and the mirrored lane of its
+// eight or sixteen for 4 and 8: the same thing once a reduction has made smaller groups of lanes
+// equal. These are lane permutations of the vector unit; a shuffle goes through LDS and takes
+// many times as long.
+template <int OFF>
+__device__ __forceinline__ void pair_bits(uint32_t v, uint32_t& a, uint32_t& b) {
+  if constexpr (OFF == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    a = r[0], b = r[1];
+  } else if constexpr (OFF == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    a = r[0], b = r[1];
+  } else {
+    // quad_perm [1,0,3,2], quad_perm [2,3,0,1], row_half_mirror, row_mirror
+    constexpr int CTRL = OFF == 1 ? 0xb1 : OFF == 2 ? 0x4e : OFF == 4 ? 0x141 : 0x140;
+    a = v, b = (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
+  }
+}
+template <int OFF, class T, class Op>
+__device__ __forceinline__ T with_partner(T v, Op op) {
+  if constexpr (sizeof(T) == 4) {
+    uint32_t a, b;
+    pair_bits<OFF>(__builtin_bit_cast(uint32_t, v), a, b);
+    return op(__builtin_bit_cast(T, a), __builtin_bit_cast(T, b));
+  } else {
+    const uint64_t bits = __builtin_bit_cast(uint64_t, v);
+    uint32_t al, bl, ah, bh;
+    pair_bits<OFF>((uint32_t)bits, al, bl);
+    pair_bits<OFF>((uint32_t)(bits >> 32), ah, bh);
+    return op(__builtin_bit_cast(T, al | (uint64_t)ah << 32),
+              __builtin_bit_cast(T, bl | (uint64_t)bh << 32));
+  }
+}
+
+// Sum, or another associative and commutative operation, over the L lanes (a power of two up to
+// 64) that share a row; every lane gets the same result.
 template <int L, class T, class Op>
 __device__ __forceinline__ T lanes_reduce(T v, Op op) {
-#pragma unroll
-  for (int off = L / 2; off >= 1; off >>= 1) v = op(v, __shfl_xor(v, off, 64));
+  if constexpr (L > 1) v = with_partner<1>(v, op);
+  if constexpr (L > 2) v = with_partner<2>(v, op);
+  if constexpr (L > 4) v = with_partner<4>(v, op);
+  if constexpr (L > 8) v = with_partner<8>(v, op);
+  if constexpr (L > 16) v = with_partner<16>(v, op);
+  if constexpr (L > 32) v = with_partner<32>(v, op);
   return v;
 }
 template <int L, class T>
