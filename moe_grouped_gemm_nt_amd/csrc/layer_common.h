@@ -54,16 +54,13 @@ __device__ __forceinline__ float from_f32<float>(float f) { return f; }
 template <>
 __device__ __forceinline__ bf16_t from_f32<bf16_t>(float f) { return bf16_t{bf16_bits(f)}; }
 
-// e^x for x <= 0 (NaN stays NaN): 2^(x log2 e) with the rounding of the product put back, so
-// that the relative error does not grow with |x|.
+// e^x for x <= 0 (0 for -inf, NaN for NaN), as 2^(x log2 e): the product's rounding is a relative
+// error of |x| 2^-24, the same as that of the difference that x usually is.
 __device__ __forceinline__ float exp_neg(float x) {
-  x = x < -150.f ? -150.f : x;  // also -inf; e^-150 is below the smallest float
-  const float t = x * 1.44269504f;
-  const float r = fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;
-  return __builtin_amdgcn_exp2f(t) * fmaf(r, 0.69314718f, 1.f);
+  return __builtin_amdgcn_exp2f(x * 1.44269504f);
 }
 
-// sigmoid(v) and 1 - sigmoid(v), each to full relative precision.
+// sigmoid(v) and 1 - sigmoid(v), each to the relative precision of exp_neg.
 __device__ __forceinline__ void sigmoid_parts(float v, float& q, float& one_minus_q) {
   const float a = exp_neg(-fabsf(v)), r = 1.f / (1.f + a);
   q = v >= 0.f ? r : a * r;
@@ -120,6 +117,34 @@ __device__ __forceinline__ T lanes_reduce(T v, Op op) {
 template <int L, class T>
 __device__ __forceinline__ T lanes_sum(T v) {
   return lanes_reduce<L>(v, [](T a, T b) { return a + b; });
+}
+
+// Inclusive prefix sum over the L lanes that share a row.
+template <int L>
+__device__ __forceinline__ int lanes_prefix(int v) {
+  static_assert(L >= 16, "whole rows of 16 lanes");
+  // row_shr 1, 2, 4, 8: zeros come in from outside the 16 lanes
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  const int lane = threadIdx.x & 63;
+  if constexpr (L >= 32) {
+    const int before = __shfl(v, (lane & 32) + 15, 64);
+    v += (lane & 16) ? before : 0;
+  }
+  if constexpr (L >= 64) {
+    const int before = __shfl(v, 31, 64);
+    v += (lane & 32) ? before : 0;
+  }
+  return v;
+}
+
+// LDS accesses of a wave take effect in program order; this keeps the program's order where
+// lanes of one wave exchange values through LDS without a barrier.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 }  // namespace mgg_layer

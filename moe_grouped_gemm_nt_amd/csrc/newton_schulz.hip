@@ -188,12 +188,7 @@ __device__ __forceinline__ int tile_of_block(int b, int tiles) {
   return b < whole ? (b & 7) * per + (b >> 3) : b;
 }
 
-// LDS accesses of a wave take effect in program order; this keeps the program's order.
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
+// The two halves of a value in one word, hi in the lower.
 __device__ __forceinline__ uint32_t pack_halves(float v) {
   _Float16 hi, lo;
   split(v, hi, lo);

@@ -8,7 +8,12 @@
 // its chunk meets and writes one partial (sum of p, counts) per chunk and sequence. Along
 // that walk chunk + sequence strictly increases, so it numbers the partials without a table.
 // A second kernel sums them in order of the chunks: float sums have one order, and the only
-// atomics are integer counters.
+// atomics on sums are integer counters.
+//
+// The forward kernel is bound by its vector operations, about 400 for four rows of 288 experts,
+// the backward one by HBM. Measured for 65536 rows of 288 float32 logits, 8 chosen, 16 sequences:
+// selection alone 22 us; with counts and losses 32 us and 5 us for the sums; backward 33 us,
+// 4.7 TB/s.
 
 #include "layer_common.h"
 
@@ -20,8 +25,9 @@ constexpr int kThreads = 256;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxExperts = 4096;
 constexpr int kMaxSequences = 65535;  // grid.y of the summing kernel
-// Workgroups that the rows of a large call are dealt to: four for each CU.
-constexpr int kRowBlocks = 1024;
+// Most workgroups that rows are dealt to: four for each CU. Selection with a bias has registers
+// for two or three on a CU and takes two.
+constexpr int kRowBlocks = 1024, kRowBlocksBias = 512;
 
 struct RouteArgs {
   const void* logits;
@@ -84,12 +90,19 @@ __device__ int sequence_of(const int32_t* ends, int S, int row, int from, int* s
   return S;
 }
 
-template <class T, int L, int V>
-__device__ __forceinline__ void load_row(const T* row, int G, int lane, float (&l)[V]) {
+// How a row is laid over lanes: L lanes, V slots each, of which the first FULL hold an expert in
+// every lane for all G that take this shape.
+template <int L_, int V_, int FULL_>
+struct ShapeOf {
+  static constexpr int L = L_, V = V_, FULL = FULL_;
+};
+
+template <class SHAPE, class T>
+__device__ __forceinline__ void load_row(const T* row, int G, int lane, float (&l)[SHAPE::V]) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    const int e = lane + L * v;
-    l[v] = e < G ? to_f32(row[e]) : -INFINITY;
+  for (int v = 0; v < SHAPE::V; ++v) {
+    const int e = lane + SHAPE::L * v;
+    l[v] = v < SHAPE::FULL || e < G ? to_f32(row[e]) : -INFINITY;
   }
 }
 
@@ -101,87 +114,213 @@ __device__ __forceinline__ float row_max(const float (&l)[V]) {
   return lanes_reduce<L>(m, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// One row: probabilities p[v] (zero for padding slots), and ids and weights written.
-// BIAS orders by q + bias in float64, where sums that float32 cannot tell apart still differ.
-template <int L, int V, bool SIGMOID, bool BIAS>
-__device__ __forceinline__ void route_row(const RouteArgs& a, int t, bool active, int lane,
-                                          const float (&l)[V], float (&p)[V], int* s_count) {
-  const Scores<SIGMOID> sc(row_max<L>(l));
-  float sum = 0.f;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    p[v] = sc.hat(l[v]);
-    sum += p[v];
-  }
-  sum = lanes_sum<L>(sum);
-  const float inv_sum = sum == 0.f ? 0.f : 1.f / sum;
+// Candidates that a row's selection keeps, in LDS, two to a lane.
+template <int L>
+constexpr int kCandidates = 2 * L;
 
-  using Key = std::conditional_t<BIAS, double, float>;
-  Key key[V];
+// The chosen of a row as a lane holds them: `id` at place `rank` (>= k: none), with its hat.
+template <int L>
+struct Chosen {
+  static constexpr int N = 2;  // places lane and lane + L; kMaxTopk <= 2 L
+  int rank[N], id[N];
+  float hat[N];
+};
+
+// Value of a lane's maximum as an integer of the same order.
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t b = __float_as_uint(f);
+  return b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u ^ ((int)u < 0 ? 0x80000000u : 0xffffffffu));
+}
+
+// Selection key of expert e: its logit, or q + bias in float64, where sums that float32 cannot
+// tell apart still differ.
+template <bool BIAS>
+using KeyOf = std::conditional_t<BIAS, double, float>;
+template <bool BIAS>
+__device__ __forceinline__ KeyOf<BIAS> key_of(float l, const float* bias, int e) {
+  if constexpr (BIAS) return 1.0 / (1.0 + exp(-(double)l)) + (double)bias[e];
+  else return l;
+}
+
+// The k first experts by key, one after another: every round takes the largest key that is left
+// (the lower index among equals; never NaN or -inf). For any row, at about 5 k V operations.
+template <int L, int V, bool BIAS, class Hat>
+__device__ __forceinline__ Chosen<L> choose_by_rounds(const RouteArgs& a, int lane,
+                                                      const float (&l)[V], Hat hat_of) {
+  using Key = KeyOf<BIAS>;
+  uint64_t taken = 0;  // slots
+  Chosen<L> c;
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if constexpr (BIAS) {
-      const int e = lane + L * v;
-      const double q = 1.0 / (1.0 + exp(-(double)l[v]));
-      key[v] = e < a.G && l[v] > -INFINITY ? q + (double)a.bias[e] : -INFINITY;
-    } else {
-      key[v] = l[v];
-    }
-  }
-  int id[kMaxTopk / L > 0 ? cdiv(kMaxTopk, L) : 1];
-  float w[kMaxTopk / L > 0 ? cdiv(kMaxTopk, L) : 1];
-  float chosen = 0.f;
+  for (int i = 0; i < c.N; ++i) c.rank[i] = lane + L * i, c.id[i] = -1, c.hat[i] = 0.f;
   for (int r = 0; r < a.k; ++r) {
     Key best = -INFINITY;
     int e = INT32_MAX;
+    float logit = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const bool more = key[v] > best;  // false for NaN and -inf; the lower index wins a tie
-      e = more ? lane + L * v : e;
-      best = more ? key[v] : best;
+      const int at = lane + L * v;
+      if (at < a.G && l[v] > -INFINITY && !(taken >> v & 1)) {
+        const Key key = key_of<BIAS>(l[v], a.bias, at);
+        if (key > best) best = key, e = at, logit = l[v];
+      }
     }
     const Key top = lanes_reduce<L>(best, [](Key x, Key y) { return x > y ? x : y; });
-    e = lanes_reduce<L>(best == top ? e : INT32_MAX, [](int x, int y) { return min(x, y); });
-    float hat = 0.f;
+    const int first = lanes_reduce<L>(best == top ? e : INT32_MAX,
+                                      [](int x, int y) { return min(x, y); });
+    if (first == INT32_MAX) break;  // the same for all lanes of the row
+    logit = __shfl(logit, first & (L - 1), L);
+    if ((first & (L - 1)) == lane) taken |= 1ull << (first / L);
+    const float hat = hat_of(logit);
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (lane + L * v == e) {
-        hat = p[v];
-        key[v] = -INFINITY;
+    for (int i = 0; i < c.N; ++i)
+      if (lane + L * i == r) c.id[i] = first, c.hat[i] = hat;
+  }
+  return c;
+}
+
+// A candidate's place in the order as one integer: by key, then by the lower index. Zeros of
+// either sign are equal.
+__device__ __forceinline__ uint64_t order_of(float key, int e) {
+  return (uint64_t)ordered(key + 0.f) << 32 | (uint32_t)~e;
+}
+
+// The same by candidates. The k-th largest of the lanes' own maxima is a bound that at least k
+// keys reach; the few that do (11 of 288 for k = 8) are gathered in LDS and ranked against each
+// other, a sixth of the work of k rounds. With a bias the bound is taken on float32 sums and
+// lowered by more than their error, and only candidates get a float64 key. Returns false where
+// the candidates do not fit (equal logits, k above the lanes): a matter of this row alone, so
+// its result does not depend on its neighbours.
+template <class T, int L, int V, bool SIGMOID, bool BIAS, class Hat>
+__device__ __forceinline__ bool choose_by_candidates(const RouteArgs& a, const T* row, int lane,
+                                                     const float (&l)[V], const float (&hat)[V],
+                                                     float to_q, Hat hat_of, int* s_id,
+                                                     uint64_t* s_order, Chosen<L>& c) {
+  auto rough = [&](int v) {  // what the bound is taken on
+    if constexpr (!BIAS) return l[v];
+    const int e = lane + L * v;
+    return e < a.G && l[v] > -INFINITY ? hat[v] * to_q + a.bias[e] : -INFINITY;
+  };
+  float most = -INFINITY;
+#pragma unroll
+  for (int v = 0; v < V; ++v) most = fmaxf(most, rough(v));
+  // lanes apart by their number in the last bits: k rounds take k lanes
+  uint32_t left = (ordered(most) & ~(uint32_t)(L - 1)) | (uint32_t)lane, bound = 0;
+  for (int r = 0; r < a.k; ++r) {
+    bound = lanes_reduce<L>(left, [](uint32_t x, uint32_t y) { return max(x, y); });
+    left = left == bound ? 0u : left;
+  }
+  // ordered(-inf) is 0x007fffff: no k lanes have anything to take
+  float least = bound <= 0x00800000u ? -INFINITY : from_ordered(bound & ~(uint32_t)(L - 1));
+  if (BIAS && least < INFINITY) least -= 4e-6f * (1.f + fabsf(least));
+  least = fmaxf(least, -3.402823466e38f);  // -inf itself is no candidate
+  using Bits = std::conditional_t<(V > 32), uint64_t, uint32_t>;
+  Bits slots = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) slots |= rough(v) >= least ? (Bits)1 << v : 0;
+  const int mine = V > 32 ? __popcll(slots) : __popc((uint32_t)slots);
+  const int upto = lanes_prefix<L>(mine);
+  const int total = __shfl(upto, L - 1, L);
+  if (total > kCandidates<L>) return false;
+  for (int at = upto - mine; slots != 0; slots &= slots - 1, ++at)
+    s_id[at] = lane + L * (V > 32 ? __ffsll((unsigned long long)slots) - 1
+                                  : __ffs((uint32_t)slots) - 1);
+  wave_order();
+  uint64_t mine_at[c.N];
+  auto take = [&](int i) {
+    const int n = lane + L * i;
+    c.rank[i] = n, c.id[i] = -1, c.hat[i] = 0.f;
+    mine_at[i] = ~0ull;
+    if (n < total) {
+      const int e = s_id[n];
+      const float logit = to_f32(row[e]);
+      c.id[i] = e;
+      c.hat[i] = hat_of(logit);
+      if constexpr (BIAS) {
+        // doubles order as integers once negative ones are turned round; equal ones are told
+        // apart by the lanes that hold them, below
+        const int64_t b = __builtin_bit_cast(int64_t, key_of<BIAS>(logit, a.bias, e) + 0.0);
+        mine_at[i] = (uint64_t)(b ^ (b >> 63 & 0x7fffffffffffffffll)) ^ 0x8000000000000000ull;
+      } else {
+        mine_at[i] = order_of(logit, e);
       }
-    hat = __shfl(hat, e & (L - 1), L);
-    if (e == INT32_MAX) hat = 0.f;
-    chosen += hat;
-    if (s_count != nullptr && active && lane == 0 && e != INT32_MAX) atomicAdd(&s_count[e], 1);
-    if ((r & (L - 1)) == lane) {
-      id[r / L] = e == INT32_MAX ? -1 : e;
-      w[r / L] = hat;
+      s_order[n] = mine_at[i];
+    }
+  };
+  auto rank = [&](int i) {
+    if (c.id[i] < 0) return;
+    int before = 0;
+#pragma unroll 4
+    for (int n = 0; n < total; ++n) {
+      const uint64_t other = s_order[n];
+      before += other > mine_at[i] ? 1 : 0;
+      if constexpr (BIAS) before += other == mine_at[i] && s_id[n] < c.id[i] ? 1 : 0;
+    }
+    c.rank[i] = before;
+  };
+  take(0);
+  take(1);
+  wave_order();
+  rank(0);
+  if (total > L) rank(1);
+  wave_order();  // the next row's candidates may come
+  return true;
+}
+
+// One row: ids and weights written, its probabilities added to `acc` where `active`.
+template <class T, class SHAPE, bool SIGMOID, bool BIAS, bool STATS>
+__device__ __forceinline__ void route_row(const RouteArgs& a, const T* row, int t, bool active,
+                                          int lane, const float (&l)[SHAPE::V],
+                                          float (&acc)[SHAPE::V], int* s_count, int* s_id,
+                                          uint64_t* s_order) {
+  constexpr int L = SHAPE::L, V = SHAPE::V;
+  const Scores<SIGMOID> sc(row_max<L>(l));
+  float hat[V], sum = 0.f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    hat[v] = sc.hat(l[v]);
+    sum += hat[v];
+  }
+  sum = lanes_sum<L>(sum);
+  const float inv_sum = sum == 0.f ? 0.f : 1.f / sum;
+  if constexpr (STATS) {
+    if (active) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(hat[v], inv_sum, acc[v]);
     }
   }
+  auto hat_of = [&](float logit) { return sc.hat(logit); };
+  Chosen<L> c;
+  if (!choose_by_candidates<T, L, V, SIGMOID, BIAS>(a, row, lane, l, hat, sc.to_q, hat_of, s_id,
+                                                    s_order, c))
+    c = choose_by_rounds<L, V, BIAS>(a, lane, l, hat_of);
+  float chosen = 0.f;
+#pragma unroll
+  for (int i = 0; i < c.N; ++i) chosen += c.rank[i] < a.k ? c.hat[i] : 0.f;
+  chosen = lanes_sum<L>(chosen);
   const float to_w =
       a.scale * (a.renormalize ? (chosen == 0.f ? 0.f : 1.f / chosen)
                                : (SIGMOID ? sc.to_q : inv_sum));
-  if (active) {
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(id) / sizeof(int)); ++i) {
-      const int r = lane + L * i;
-      if (r < a.k) {
-        a.ids[(size_t)t * a.k + r] = id[i];
-        a.weights[(size_t)t * a.k + r] = id[i] < 0 ? 0.f : w[i] * to_w;
-      }
+  for (int i = 0; i < c.N; ++i)
+    if (active && c.rank[i] < a.k) {
+      a.ids[(size_t)t * a.k + c.rank[i]] = c.id[i];
+      a.weights[(size_t)t * a.k + c.rank[i]] = c.id[i] < 0 ? 0.f : c.hat[i] * to_w;
+      if (STATS && c.id[i] >= 0) atomicAdd(&s_count[c.id[i]], 1);
     }
-  }
-#pragma unroll
-  for (int v = 0; v < V; ++v) p[v] *= inv_sum;
 }
 
-template <class T, int L, int V, bool SIGMOID, bool BIAS, bool STATS>
+template <class T, class SHAPE, bool SIGMOID, bool BIAS, bool STATS>
 __global__ __launch_bounds__(kThreads) void route_rows(RouteArgs a) {
   extern __shared__ int s_dyn[];  // STATS: counts [G], sums [G]
   __shared__ int s_found[kThreads / 64];
+  constexpr int L = SHAPE::L, V = SHAPE::V, RP = kThreads / L;  // RP rows at once
+  __shared__ uint64_t s_order[RP][kCandidates<L>];
+  __shared__ int s_id[RP][kCandidates<L>];
   int* s_count = STATS ? s_dyn : nullptr;
   float* s_prob = reinterpret_cast<float*>(s_dyn + a.G);
-  constexpr int RP = kThreads / L;  // rows at once
   const int lane = threadIdx.x & (L - 1), grp = threadIdx.x / L;
   const int r0 = blockIdx.x * a.rows_per_block;
   const int r1 = min(a.T, r0 + a.rows_per_block);
@@ -207,27 +346,31 @@ __global__ __launch_bounds__(kThreads) void route_rows(RouteArgs a) {
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] = 0.f;
     }
+    auto row_at = [&](int t) {
+      return reinterpret_cast<const T*>(a.logits) + (size_t)min(t, end - 1) * a.ld;
+    };
     for (int base = row; base < end; base += RP) {
       const int t = base + grp;
-      const bool active = t < end;
-      float l[V], p[V];
-      load_row<T, L>(reinterpret_cast<const T*>(a.logits) + (size_t)min(t, end - 1) * a.ld,
-                     a.G, lane, l);
-      route_row<L, V, SIGMOID, BIAS>(a, t, active, lane, l, p, s_count);
-      if constexpr (STATS) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] += active ? p[v] : 0.f;
-      }
+      float l[V];
+      load_row<SHAPE>(row_at(t), a.G, lane, l);
+      route_row<T, SHAPE, SIGMOID, BIAS, STATS>(a, row_at(t), t, t < end, lane, l, acc, s_count,
+                                                s_id[grp], s_order[grp]);
     }
     if constexpr (STATS) {
-      // the groups' sums, added in the order of the groups
-      for (int g = 0; g < RP; ++g) {
+      // the sums of a wave's rows, then those of the waves one after another
+      const auto add = [](float x, float y) { return x + y; };
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (L <= 16) acc[v] = with_partner<16>(acc[v], add);
+        if constexpr (L <= 32) acc[v] = with_partner<32>(acc[v], add);
+      }
+      for (int w = 0; w < kThreads / 64; ++w) {
         __syncthreads();
-        if (grp == g) {
+        if ((int)threadIdx.x / 64 == w && (threadIdx.x & 63) < L) {
 #pragma unroll
           for (int v = 0; v < V; ++v) {
             const int e = lane + L * v;
-            if (e < a.G) s_prob[e] = g == 0 ? acc[v] : s_prob[e] + acc[v];
+            if (e < a.G) s_prob[e] = w == 0 ? acc[v] : s_prob[e] + acc[v];
           }
         }
       }
@@ -275,6 +418,7 @@ __global__ __launch_bounds__(kThreads) void route_balance(RouteArgs a, int32_t* 
   int count = 0;
   if (end > start && e < a.G) {
     const int last = (end - 1) / a.rows_per_block;
+#pragma unroll 8
     for (int c = start / a.rows_per_block + strip; c <= last; c += kSumStrips) {
       const size_t slot = (size_t)(c + s) * a.G + e;
       prob += (double)a.part_prob[slot];
@@ -284,28 +428,39 @@ __global__ __launch_bounds__(kThreads) void route_balance(RouteArgs a, int32_t* 
   s_prob[strip][col] = prob;
   s_count[strip][col] = count;
   __syncthreads();
+  if (threadIdx.x >= 64) return;
+  double dot = 0.0;
   if (threadIdx.x < kSumCols) {
     for (int i = 1; i < kSumStrips; ++i) {
       prob += s_prob[i][col];
       count += s_count[i][col];
     }
     if (e < a.G) counts[(size_t)s * a.G + e] = count;
-    const double dot = lanes_sum<kSumCols>((double)count * prob);
-    if (threadIdx.x == 0) {
-      double* at = dots + (size_t)s * gridDim.x;
-      __hip_atomic_store(at + blockIdx.x, dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      const int done = __hip_atomic_fetch_add(a.counters + s, 1, __ATOMIC_ACQ_REL,
-                                              __HIP_MEMORY_SCOPE_AGENT);
-      if (done == (int)gridDim.x - 1) {
-        double sum = 0.0;
-        for (unsigned i = 0; i < gridDim.x; ++i)
-          sum += __hip_atomic_load(at + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int n = end - start;
-        const double nn = (double)n * (double)n;
-        balance[s] = n > 0 ? (float)(sum * ((double)a.G / (double)a.k) / nn) : 0.f;
-        tokens[s] = n;
-      }
-    }
+    dot = (double)count * prob;
+  }
+  dot = lanes_sum<64>(dot);
+  // The dot goes out by an exchange whose answer has to be back before the count goes up, and is
+  // read by atomic loads: all of them act where the whole device sees them, and nothing else
+  // passes between the workgroups. (A release of the agent scope writes back the die's whole
+  // L2 instead, 5 us here.)
+  double* at = dots + (size_t)s * gridDim.x;
+  int done = 0;
+  if (threadIdx.x == 0) {
+    const double before = __hip_atomic_exchange(at + blockIdx.x, dot, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::"v"(before) : "memory");
+    done = __hip_atomic_fetch_add(a.counters + s, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (__builtin_amdgcn_readfirstlane(done) != (int)gridDim.x - 1) return;
+  double sum = 0.0;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += 64)
+    sum += __hip_atomic_load(at + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  sum = lanes_sum<64>(sum);
+  if (threadIdx.x == 0) {
+    const int n = end - start;
+    const double nn = (double)n * (double)n;
+    balance[s] = n > 0 ? (float)(sum * ((double)a.G / (double)a.k) / nn) : 0.f;
+    tokens[s] = n;
   }
 }
 
@@ -330,11 +485,19 @@ struct RouteGradArgs {
 // shares of the chosen (Q the sum of their hats),
 //   renormalised: scale * pi * (dw - sum pi dw)    [(1 - q) for sigmoid]
 //   otherwise:    scale * dw enters b (softmax), or scale * dw q (1 - q) (sigmoid).
-template <class T, int L, int V, bool SIGMOID>
+template <class T, class SHAPE, bool SIGMOID>
 __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
   __shared__ int s_found[kThreads / 64];
-  constexpr int RP = kThreads / L;
+  constexpr int L = SHAPE::L, V = SHAPE::V, RP = kThreads / L;
+  constexpr uint32_t kNone = 0xffffffffu;  // a NaN that no gradient is stored as
+  // rows 16 words apart modulo the 64 banks
+  __shared__ uint32_t s_dw[RP][L * V + (L < 64 ? 16 : 0)];
   const int lane = threadIdx.x & (L - 1), grp = threadIdx.x / L;
+  if (a.d_weights != nullptr) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_dw[grp][lane + L * v] = kNone;
+    wave_order();
+  }
   const int r0 = blockIdx.x * a.rows_per_block;
   const int r1 = min(a.T, r0 + a.rows_per_block);
   T* out = reinterpret_cast<T*>(a.d_logits);
@@ -360,26 +523,56 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
       b0[v] = a.d_balance != nullptr && e < a.G
                   ? per_count * (float)a.counts[(size_t)s * a.G + e] : 0.f;
     }
+    // a row's inputs: its logits, and the lane's share of its choices
+    struct Row {
+      float l[V];
+      int id[2];
+      float dw[2];
+    };
+    auto load = [&](int t) {
+      Row r;
+      const size_t tr = (size_t)min(t, end - 1);
+      load_row<SHAPE>(reinterpret_cast<const T*>(a.logits) + tr * a.ld, a.G, lane, r.l);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = lane + L * i;
+        const bool is = a.d_weights != nullptr && j < a.k;
+        r.id[i] = is ? a.ids[tr * a.k + j] : -1;
+        r.dw[i] = is ? a.d_weights[tr * a.k + j] : 0.f;
+      }
+      return r;
+    };
+    Row next = load(row + grp);
     for (int base = row; base < end; base += RP) {
       const int t = base + grp;
       const bool active = t < end;
       const size_t tr = (size_t)min(t, end - 1);
-      float l[V], h[V], g[V];
-      load_row<T, L>(reinterpret_cast<const T*>(a.logits) + tr * a.ld, a.G, lane, l);
-#pragma unroll
-      for (int v = 0; v < V; ++v) g[v] = 0.f;
+      const Row in = next;
+      if (base + RP < end) next = load(t + RP);
+      const float(&l)[V] = in.l;
+      float h[V], g[V];
       uint64_t chosen = 0;  // bit v: slot v is among the row's choices
       if (a.d_weights != nullptr) {
-        for (int r = 0; r < a.k; ++r) {
-          const int id = a.ids[tr * a.k + r];
-          const float dw = a.d_weights[tr * a.k + r];
+        // the gradients go to their experts' lanes through LDS, which holds kNone elsewhere
 #pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const bool is = lane + L * v == id && id < a.G;
-            g[v] = is ? dw : g[v];
-            chosen |= is ? 1ull << v : 0;
-          }
+        for (int i = 0; i < 2; ++i)
+          if ((unsigned)in.id[i] < (unsigned)a.G)
+            s_dw[grp][in.id[i]] = in.dw[i] != in.dw[i] ? 0x7fc00000u : __float_as_uint(in.dw[i]);
+        wave_order();
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const uint32_t bits = s_dw[grp][lane + L * v];
+          g[v] = __uint_as_float(bits);
+          chosen |= bits != kNone ? 1ull << v : 0;
         }
+        wave_order();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if ((unsigned)in.id[i] < (unsigned)a.G) s_dw[grp][in.id[i]] = kNone;
+        wave_order();
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) g[v] = 0.f;
       }
       const Scores<SIGMOID> sc(row_max<L>(l));
       float sum = 0.f, q_sum = 0.f, q_dw = 0.f;
@@ -412,7 +605,7 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
         const int e = lane + L * v;
         float d = h[v] * ((b0[v] - mean_b) * inv_sum + g[v]);
         if constexpr (SIGMOID) d *= Scores<SIGMOID>::one_minus_q(l[v]);
-        if (active && e < a.G) out[tr * a.G + e] = from_f32<T>(d);
+        if (active && (v < SHAPE::FULL || e < a.G)) out[tr * a.G + e] = from_f32<T>(d);
       }
     }
     row = end;
@@ -422,37 +615,35 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
 }
 
 // Rows a workgroup takes: whole passes of kThreads / L rows, and no more workgroups than
-// kRowBlocks, so that partials stay few next to the logits.
-int rows_per_block(int T, int G) {
+// `most`, so that partials stay few next to the logits.
+int rows_per_block(int T, int G, int most) {
   const int pass = G <= 320 ? 16 : G <= 512 ? 8 : 4;
-  const int per = cdiv(T > 0 ? T : 1, kRowBlocks);
+  const int per = cdiv(T > 0 ? T : 1, most);
   return cdiv(per, pass) * pass;
 }
-int row_blocks(int T, int G) { return T > 0 ? cdiv(T, rows_per_block(T, G)) : 1; }
+int row_blocks(int T, int rows) { return T > 0 ? cdiv(T, rows) : 1; }
 
-// Calls f(L, V) as compile-time constants: the fewest slots that hold G. Up to 320 experts 16
-// lanes share a row (four rows to a wave); beyond that a row takes more lanes, so that its
-// logits still fit the registers.
+// Calls f with the shape that holds G in the fewest slots. Up to 320 experts 16 lanes share a row
+// (four rows to a wave); beyond that a row takes more lanes, so that its logits still fit the
+// registers.
 template <class F>
 void with_shape(int G, F f) {
-  using std::integral_constant;
-#define MGG_SHAPE(MAX, L, V) \
-  if (G <= MAX) return f(integral_constant<int, L>{}, integral_constant<int, V>{})
-  MGG_SHAPE(64, 16, 4);
-  MGG_SHAPE(128, 16, 8);
-  MGG_SHAPE(256, 16, 16);
-  MGG_SHAPE(320, 16, 20);
-  MGG_SHAPE(512, 32, 16);
-  MGG_SHAPE(1024, 64, 16);
-  MGG_SHAPE(2048, 64, 32);
-  MGG_SHAPE(4096, 64, 64);
-#undef MGG_SHAPE
+  if (G <= 64) return f(ShapeOf<16, 4, 0>{});
+  if (G <= 128) return f(ShapeOf<16, 8, 4>{});
+  if (G <= 192) return f(ShapeOf<16, 12, 8>{});
+  if (G <= 256) return f(ShapeOf<16, 16, 12>{});
+  if (G <= 288) return f(ShapeOf<16, 18, 16>{});
+  if (G <= 320) return f(ShapeOf<16, 20, 18>{});
+  if (G <= 512) return f(ShapeOf<32, 16, 10>{});
+  if (G <= 1024) return f(ShapeOf<64, 16, 8>{});
+  if (G <= 2048) return f(ShapeOf<64, 32, 16>{});
+  f(ShapeOf<64, 64, 32>{});
 }
 
 struct Workspace {
   size_t prob, count, dots, counters, bytes;
   Workspace(int T, int G, int S) {
-    const size_t slots = (size_t)row_blocks(T, G) + S;
+    const size_t slots = (size_t)row_blocks(T, rows_per_block(T, G, kRowBlocks)) + S;
     prob = 0;
     count = round_up(prob + slots * G * 4, 256);
     dots = round_up(count + slots * G * 4, 256);
@@ -505,8 +696,9 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
     return fail(MGG_EINVAL, "counts, tokens and balance are given together");
   if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(balance, 4))
     return fail(MGG_EINVAL, "counts, tokens and balance must be 4-byte aligned");
-  RouteArgs a{logits, ld,       bias, T,       G,          k,       S, renormalize,
-              scale,  seq_ends, ids,  weights, rows_per_block(T, G), nullptr, nullptr, nullptr};
+  const int rows = rows_per_block(T, G, bias ? kRowBlocksBias : kRowBlocks);
+  RouteArgs a{logits, ld,       bias, T,       G,    k,       S,       renormalize,
+              scale,  seq_ends, ids,  weights, rows, nullptr, nullptr, nullptr};
   double* dots = nullptr;
   if (stats) {
     const Workspace ws(T, G, S);
@@ -521,12 +713,13 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
   } else if (T == 0) {
     return MGG_OK;
   }
-  const dim3 grid((unsigned)row_blocks(T, G));
+  const dim3 grid((unsigned)row_blocks(T, rows));
   const size_t lds = stats ? (size_t)G * 8 : 0;
   const bool sigmoid = score == MGG_SCORE_SIGMOID;
-  with_shape(G, [&](auto L, auto V) {
+  with_shape(G, [&](auto shape) {
+    using SHAPE = decltype(shape);
     auto go = [&](auto elem, auto sig, auto biased, auto with_stats) {
-      route_rows<decltype(elem), L(), V(), sig(), biased(), with_stats()>
+      route_rows<decltype(elem), SHAPE, sig(), biased(), with_stats()>
           <<<grid, kThreads, lds, stream>>>(a);
     };
     auto by_stats = [&](auto elem, auto sig, auto biased) {
@@ -567,16 +760,17 @@ mgg_status route_topk_backward(mgg_act dt, int T, int G, int k, const void* logi
       !aligned(d_balance, 4))
     return fail(MGG_EINVAL, "ids, counts, tokens and gradients must be 4-byte aligned");
   if (T == 0) return MGG_OK;
-  const RouteGradArgs a{logits, ld,     T,      G,         k,         S,        renormalize,
-                        scale,  seq_ends, ids,  counts,    tokens,    d_weights, d_balance,
-                        d_logits, rows_per_block(T, G)};
-  const dim3 grid((unsigned)row_blocks(T, G));
-  with_shape(G, [&](auto L, auto V) {
+  const int rows = rows_per_block(T, G, kRowBlocks);
+  const RouteGradArgs a{logits,   ld,  T,      G,      k,         S,         renormalize, scale,
+                        seq_ends, ids, counts, tokens, d_weights, d_balance, d_logits,    rows};
+  const dim3 grid((unsigned)row_blocks(T, rows));
+  with_shape(G, [&](auto shape) {
+    using SHAPE = decltype(shape);
     auto by_score = [&](auto elem) {
       if (score == MGG_SCORE_SIGMOID)
-        route_grad<decltype(elem), L(), V(), true><<<grid, kThreads, 0, stream>>>(a);
+        route_grad<decltype(elem), SHAPE, true><<<grid, kThreads, 0, stream>>>(a);
       else
-        route_grad<decltype(elem), L(), V(), false><<<grid, kThreads, 0, stream>>>(a);
+        route_grad<decltype(elem), SHAPE, false><<<grid, kThreads, 0, stream>>>(a);
     };
     if (dt == MGG_ACT_BF16) by_score(bf16_t{});
     else by_score(0.f);
