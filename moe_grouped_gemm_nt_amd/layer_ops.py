@@ -60,6 +60,50 @@ def declare(lib: ctypes.CDLL):
         f.restype = sz
 
 
+def _ptr(t):
+    """Address of a tensor, None for none (ctypes takes either for a pointer)."""
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(first, *rest):
+    """Every tensor that is given on the first one's GPU."""
+    device = first.device
+    ok = device.type == "cuda"
+    for t in rest:
+        if t is not None and t.device != device:
+            ok = False
+    _mgg._require(ok, "all tensors must be on the same GPU")
+    return device
+
+
+_raw_stream = None
+
+
+def _current_stream(index) -> int:
+    """Handle of the device's current stream; without the Stream object where torch offers
+    that (a tenth of the time of a small call)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
+    return _raw_stream(index)
+
+
+def _run(fn, device, *args):
+    """Calls an entry point on the device's current stream, and raises on a non-OK status. The
+    device is made current only when it is not: small calls are bound by this host code."""
+    import torch
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _current_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _current_stream(index))
+    if status:
+        _mgg._check(status)
+
+
 def _act(t, name) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -71,22 +115,26 @@ def _act(t, name) -> int:
 
 def _rows(t, T, H, dtype, name) -> int:
     """Row stride of a [T, H] tensor that is read."""
-    _mgg._require(tuple(t.shape) == (T, H), f"{name} must be [{T}, {H}], got {list(t.shape)}")
-    _mgg._require(t.dtype == dtype, f"{name} must be {dtype}, got {t.dtype}")
-    _mgg._require(H <= 1 or t.stride(1) == 1, f"{name} must have contiguous rows")
+    if t.shape != (T, H):
+        raise ValueError(f"{name} must be [{T}, {H}], got {list(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    row, col = t.stride()
+    if H > 1 and col != 1:
+        raise ValueError(f"{name} must have contiguous rows")
     if T <= 1:
         return H
-    _mgg._require(t.stride(0) >= H, f"{name}: rows must not overlap")
-    return t.stride(0)
+    if row < H:
+        raise ValueError(f"{name}: rows must not overlap")
+    return row
 
 
 def _given(t, shape, dtype, name, like):
     """An output: the caller's, checked, or a new one."""
-    import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    _mgg._require(tuple(t.shape) == tuple(shape) and t.dtype == dtype,
-                  f"{name} must be {dtype} {list(shape)}")
+        return like.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}")
     _mgg._contig(t)
     return t
 
@@ -94,9 +142,9 @@ def _given(t, shape, dtype, name, like):
 def _workspace(ws, size, like):
     import torch
     if ws is None:
-        return torch.empty(size, dtype=torch.uint8, device=like.device)
-    _mgg._require(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.numel() >= size,
-                  f"workspace must be a contiguous uint8 tensor of at least {size} bytes")
+        return like.new_empty(size, dtype=torch.uint8)
+    if ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < size:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {size} bytes")
     return ws
 
 
@@ -111,7 +159,8 @@ def _sequences(seq_ends):
 
 
 def _score_code(score) -> int:
-    _mgg._require(score in _SCORE, f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    if score not in _SCORE:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
     return _SCORE[score]
 
 
@@ -132,27 +181,24 @@ def route_topk(logits, topk, bias=None, seq_ends=None, score="softmax", renormal
     S = _sequences(seq_ends)
     if bias is not None:
         _mgg._require(code == MGG_SCORE_SIGMOID, "a selection bias goes with sigmoid scores")
-        _mgg._require(bias.dtype == torch.float32 and tuple(bias.shape) == (G,),
+        _mgg._require(bias.dtype == torch.float32 and bias.shape == (G,),
                       "bias must be float32 [G]")
         _mgg._contig(bias)
     lib = _mgg.load_library()
-    _mgg._same_device(logits, bias, seq_ends, workspace)
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    _same_device(logits, bias, seq_ends, workspace)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    weights = logits.new_empty((T, k), dtype=torch.float32)
     counts = tokens = loss = None
     size = 0
     if balance:
-        counts = torch.empty((S, G), dtype=torch.int32, device=logits.device)
-        tokens = torch.empty(S, dtype=torch.int32, device=logits.device)
-        loss = torch.empty(S, dtype=torch.float32, device=logits.device)
+        counts = logits.new_empty((S, G), dtype=torch.int32)
+        tokens = logits.new_empty(S, dtype=torch.int32)
+        loss = logits.new_empty(S, dtype=torch.float32)
         size = lib.route_topk_workspace(T, G, S)
         workspace = _workspace(workspace, size, logits)
-    with torch.cuda.device(logits.device):
-        _mgg._check(lib.route_topk(
-            dt, T, G, k, _mgg._ptr(logits), ld, _mgg._ptr(bias), code, int(bool(renormalize)),
-            float(scale), S, _mgg._ptr(seq_ends), _mgg._ptr(ids), _mgg._ptr(weights),
-            _mgg._ptr(counts), _mgg._ptr(tokens), _mgg._ptr(loss),
-            _mgg._ptr(workspace) if balance else None, size, _mgg._stream(logits.device)))
+    _run(lib.route_topk, logits.device, dt, T, G, k, _ptr(logits), ld, _ptr(bias), code,
+         int(bool(renormalize)), float(scale), S, _ptr(seq_ends), _ptr(ids), _ptr(weights),
+         _ptr(counts), _ptr(tokens), _ptr(loss), _ptr(workspace) if balance else None, size)
     return (ids, weights, counts, tokens, loss) if balance else (ids, weights)
 
 
@@ -175,42 +221,42 @@ def route_topk_backward(logits, ids, counts=None, tokens=None, d_weights=None, d
     _mgg._require(d_weights is not None or d_balance is not None,
                   "one of d_weights and d_balance must be given")
     if d_weights is not None:
-        _mgg._require(d_weights.dtype == torch.float32 and tuple(d_weights.shape) == (T, k),
+        _mgg._require(d_weights.dtype == torch.float32 and d_weights.shape == (T, k),
                       "d_weights must be float32 [T, k]")
     if d_balance is not None:
-        _mgg._require(d_balance.dtype == torch.float32 and tuple(d_balance.shape) == (S,),
+        _mgg._require(d_balance.dtype == torch.float32 and d_balance.shape == (S,),
                       "d_balance must be float32 [S]")
         _mgg._require(counts is not None and tokens is not None,
                       "d_balance needs counts and tokens")
-        _mgg._require(counts.dtype == torch.int32 and tuple(counts.shape) == (S, G),
+        _mgg._require(counts.dtype == torch.int32 and counts.shape == (S, G),
                       "counts must be int32 [S, G]")
-        _mgg._require(tokens.dtype == torch.int32 and tuple(tokens.shape) == (S,),
+        _mgg._require(tokens.dtype == torch.int32 and tokens.shape == (S,),
                       "tokens must be int32 [S]")
     else:
         counts = tokens = None
     lib = _mgg.load_library()
-    _mgg._same_device(logits, ids, counts, tokens, d_weights, d_balance, seq_ends, d_logits)
+    _same_device(logits, ids, counts, tokens, d_weights, d_balance, seq_ends, d_logits)
     _mgg._contig(ids, counts, tokens, d_weights, d_balance)
     d_logits = _given(d_logits, (T, G), logits.dtype, "d_logits", logits)
-    with torch.cuda.device(logits.device):
-        _mgg._check(lib.route_topk_backward(
-            dt, T, G, k, _mgg._ptr(logits), ld, code, int(bool(renormalize)), float(scale), S,
-            _mgg._ptr(seq_ends), _mgg._ptr(ids), _mgg._ptr(counts), _mgg._ptr(tokens),
-            _mgg._ptr(d_weights), _mgg._ptr(d_balance), _mgg._ptr(d_logits),
-            _mgg._stream(logits.device)))
+    _run(lib.route_topk_backward, logits.device, dt, T, G, k, _ptr(logits), ld, code,
+         int(bool(renormalize)), float(scale), S, _ptr(seq_ends), _ptr(ids), _ptr(counts),
+         _ptr(tokens), _ptr(d_weights), _ptr(d_balance), _ptr(d_logits))
     return d_logits
 
 
 def _param(params, H):
     """Element type of the parameter vectors that are given (one for all)."""
-    dtypes = {p.dtype for p in params if p is not None}
-    _mgg._require(len(dtypes) <= 1, "scale, w_after and w_before must have one element type")
+    dtype = None
     for p in params:
-        if p is not None:
-            _mgg._require(tuple(p.shape) == (H,), f"scale and norm weights must be [{H}]")
-            _mgg._contig(p)
-    return next((_act(p, "scale and norm weights") for p in params if p is not None),
-                MGG_ACT_F32)
+        if p is None:
+            continue
+        if p.shape != (H,) or not p.is_contiguous():
+            raise ValueError(f"scale and norm weights must be contiguous and must be [{H}]")
+        if dtype is not None and p.dtype != dtype:
+            raise ValueError("scale, w_after and w_before must have one element type")
+        if dtype is None:
+            dtype, code = p.dtype, _act(p, "scale and norm weights")
+    return MGG_ACT_F32 if dtype is None else code
 
 
 def _block(x, y, w_after, gate, scale, w_before, alpha, beta, eps):
@@ -225,8 +271,8 @@ def _block(x, y, w_after, gate, scale, w_before, alpha, beta, eps):
         if gate.dim() == 2:
             kind, ld_gate = MGG_GATE_ELEMENT, _rows(gate, T, H, x.dtype, "gate")
         else:
-            _mgg._require(tuple(gate.shape) == (T,) and gate.dtype == x.dtype,
-                          f"gate must be {x.dtype} [T] or [T, H]")
+            if gate.shape != (T,) or gate.dtype != x.dtype:
+                raise ValueError(f"gate must be {x.dtype} [T] or [T, H]")
             kind, ld_gate = MGG_GATE_TOKEN, gate.stride(0) if T > 1 else 1
             _mgg._require(ld_gate >= 1, "gate: values must not overlap")
     param = _param((scale, w_after, w_before), H)
@@ -245,11 +291,9 @@ def block_norm(x, w, eps=1e-6, u=None):
     T, H = x.shape
     dt, ldx, param = _act(x, "x"), _rows(x, T, H, x.dtype, "x"), _param((w,), H)
     lib = _mgg.load_library()
-    _mgg._same_device(x, w, u)
+    _same_device(x, w, u)
     u = _given(u, (T, H), x.dtype, "u", x)
-    with torch.cuda.device(x.device):
-        _mgg._check(lib.block_norm(dt, param, T, H, _mgg._ptr(x), ldx, _mgg._ptr(w), float(eps),
-                                   _mgg._ptr(u), _mgg._stream(x.device)))
+    _run(lib.block_norm, x.device, dt, param, T, H, _ptr(x), ldx, _ptr(w), float(eps), _ptr(u))
     return u
 
 
@@ -263,16 +307,13 @@ def block_norm_backward(x, w, d_u, d_x=None, eps=1e-6, workspace=None):
     ld_du = _rows(d_u, T, H, x.dtype, "d_u")
     ld_dx = _rows(d_x, T, H, x.dtype, "d_x") if d_x is not None else H
     lib = _mgg.load_library()
-    _mgg._same_device(x, w, d_u, d_x, workspace)
-    d_in = torch.empty((T, H), dtype=x.dtype, device=x.device)
-    d_w = torch.empty(H, dtype=torch.float32, device=x.device)
+    _same_device(x, w, d_u, d_x, workspace)
+    d_in = x.new_empty((T, H), dtype=x.dtype)
+    d_w = x.new_empty(H, dtype=torch.float32)
     size = lib.block_residual_norm_backward_workspace(T, H)
     workspace = _workspace(workspace, size, x)
-    with torch.cuda.device(x.device):
-        _mgg._check(lib.block_norm_backward(
-            dt, param, T, H, _mgg._ptr(x), ldx, _mgg._ptr(w), float(eps), _mgg._ptr(d_x), ld_dx,
-            _mgg._ptr(d_u), ld_du, _mgg._ptr(d_in), _mgg._ptr(d_w), _mgg._ptr(workspace), size,
-            _mgg._stream(x.device)))
+    _run(lib.block_norm_backward, x.device, dt, param, T, H, _ptr(x), ldx, _ptr(w), float(eps),
+         _ptr(d_x), ld_dx, _ptr(d_u), ld_du, _ptr(d_in), _ptr(d_w), _ptr(workspace), size)
     return d_in, d_w
 
 
@@ -286,15 +327,13 @@ def block_residual_norm(x, y, w_after=None, gate=None, scale=None, w_before=None
     block = _block(x, y, w_after, gate, scale, w_before, alpha, beta, eps)
     T, H = x.shape
     lib = _mgg.load_library()
-    _mgg._same_device(x, y, w_after, gate, scale, w_before, x_out, u)
+    _same_device(x, y, w_after, gate, scale, w_before, x_out, u)
     x_out = _given(x_out, (T, H), x.dtype, "x_out", x)
     if w_before is not None:
         u = _given(u, (T, H), x.dtype, "u", x)
     else:
         _mgg._require(u is None, "u and w_before go together")
-    with torch.cuda.device(x.device):
-        _mgg._check(lib.block_residual_norm(ctypes.byref(block), _mgg._ptr(x_out), _mgg._ptr(u),
-                                            _mgg._stream(x.device)))
+    _run(lib.block_residual_norm, x.device, ctypes.byref(block), _ptr(x_out), _ptr(u))
     return x_out, u
 
 
@@ -313,23 +352,21 @@ def block_residual_norm_backward(x_out, y, d_x=None, d_u=None, w_after=None, gat
     ld_dx = _rows(d_x, T, H, x_out.dtype, "d_x") if d_x is not None else H
     ld_du = _rows(d_u, T, H, x_out.dtype, "d_u") if d_u is not None else H
     lib = _mgg.load_library()
-    _mgg._same_device(x_out, y, d_x, d_u, w_after, gate, scale, w_before, workspace)
+    _same_device(x_out, y, d_x, d_u, w_after, gate, scale, w_before, workspace)
 
     def like(t, shape, dtype):
-        return None if t is None else torch.empty(shape, dtype=dtype, device=x_out.device)
+        return None if t is None else x_out.new_empty(shape, dtype=dtype)
 
-    d_in = torch.empty((T, H), dtype=x_out.dtype, device=x_out.device)
-    d_y = torch.empty((T, H), dtype=x_out.dtype, device=x_out.device)
+    d_in = x_out.new_empty((T, H), dtype=x_out.dtype)
+    d_y = x_out.new_empty((T, H), dtype=x_out.dtype)
     d_gate = None if gate is None else like(gate, tuple(gate.shape), x_out.dtype)
     d_scale, d_w_after, d_w_before = (like(p, (H,), torch.float32)
                                       for p in (scale, w_after, w_before))
     size = lib.block_residual_norm_backward_workspace(T, H)
     workspace = _workspace(workspace, size, x_out)
-    with torch.cuda.device(x_out.device):
-        _mgg._check(lib.block_residual_norm_backward(
-            ctypes.byref(block), _mgg._ptr(d_x), ld_dx, _mgg._ptr(d_u), ld_du, _mgg._ptr(d_in),
-            _mgg._ptr(d_y), _mgg._ptr(d_gate), _mgg._ptr(d_scale), _mgg._ptr(d_w_after),
-            _mgg._ptr(d_w_before), _mgg._ptr(workspace), size, _mgg._stream(x_out.device)))
+    _run(lib.block_residual_norm_backward, x_out.device, ctypes.byref(block), _ptr(d_x), ld_dx,
+         _ptr(d_u), ld_du, _ptr(d_in), _ptr(d_y), _ptr(d_gate), _ptr(d_scale), _ptr(d_w_after),
+         _ptr(d_w_before), _ptr(workspace), size)
     return d_in, d_y, d_gate, d_scale, d_w_after, d_w_before
 
 
@@ -352,14 +389,11 @@ def grouped_newton_schulz(X, out=None, steps=5, coeffs=(3.4445, -4.7750, 2.0315)
     flat = (ctypes.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
     out_dtype = out.dtype if out is not None else (out_dtype or X.dtype)
     lib = _mgg.load_library()
-    _mgg._same_device(X, out, workspace)
+    _same_device(X, out, workspace)
     _mgg._contig(X)
     out = _given(out, (G, M, N), out_dtype, "out", X)
     size = lib.grouped_newton_schulz_workspace(G, M, N)
     workspace = _workspace(workspace, size, X)
-    with torch.cuda.device(X.device):
-        _mgg._check(lib.grouped_newton_schulz(dt, _act(out, "out"), G, M, N, _mgg._ptr(X),
-                                              _mgg._ptr(out), steps, flat, float(eps),
-                                              float(scale), _mgg._ptr(workspace), size,
-                                              _mgg._stream(X.device)))
+    _run(lib.grouped_newton_schulz, X.device, dt, _act(out, "out"), G, M, N, _ptr(X), _ptr(out),
+         steps, flat, float(eps), float(scale), _ptr(workspace), size)
     return out
