@@ -505,7 +505,7 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_backward(NormArgs a) 
   if (BLOCK != 0 && a.part_block != nullptr) write_sums(c_block, a.part_block);
 }
 
-constexpr int kSumCols = 16, kSumStrips = 16;
+constexpr int kSumCols = 16, kSumStrips = 64, kSumFold = 8;
 
 // Adds the workgroups' column sums. blockIdx.y: 0 the norm before, 1 the block's.
 __global__ __launch_bounds__(kSumCols* kSumStrips) void norm_column_sums(
@@ -521,8 +521,18 @@ __global__ __launch_bounds__(kSumCols* kSumStrips) void norm_column_sums(
     for (int g = strip; g < blocks; g += kSumStrips) sum += (double)part[(size_t)g * a.H + c];
   s_part[strip][col] = sum;
   __syncthreads();
+  if (strip < kSumStrips / kSumFold) {
+    sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < kSumFold; ++i) sum += s_part[strip * kSumFold + i][col];
+  }
+  __syncthreads();
+  if (strip < kSumStrips / kSumFold) s_part[strip][col] = sum;
+  __syncthreads();
   if (strip != 0 || c >= a.H) return;
-  for (int i = 1; i < kSumStrips; ++i) sum += s_part[i][col];
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kSumStrips / kSumFold; ++i) sum += s_part[i][col];
   if (blockIdx.y == 0) {
     d_w_before[c] = (float)sum;
     return;
