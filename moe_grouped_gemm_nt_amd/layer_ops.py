@@ -76,41 +76,47 @@ def _same_device(first, *rest):
     return device
 
 
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
-def _current_stream(index) -> int:
-    """Handle of the device's current stream; without the Stream object where torch offers
-    that (a tenth of the time of a small call)."""
-    global _raw_stream
-    if _raw_stream is None:
-        import torch
-        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-            lambda i: torch.cuda.current_stream(i).cuda_stream)
-    return _raw_stream(index)
+def _torch_calls():
+    """Looks up, once, the current device and the handle of its current stream (without a Stream
+    object where torch offers that: a tenth of the time of a small call)."""
+    global _raw_stream, _current_device
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _current_device = torch.cuda.current_device
 
 
 def _run(fn, device, *args):
     """Calls an entry point on the device's current stream, and raises on a non-OK status. The
     device is made current only when it is not: small calls are bound by this host code."""
-    import torch
+    if _raw_stream is None:
+        _torch_calls()
     index = device.index
-    if torch.cuda.current_device() == index:
-        status = fn(*args, _current_stream(index))
+    if _current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
+        import torch
         with torch.cuda.device(index):
-            status = fn(*args, _current_stream(index))
+            status = fn(*args, _raw_stream(index))
     if status:
         _mgg._check(status)
 
 
+_ACTS = {}  # torch element type -> mgg_act, filled when torch is first needed
+
+
 def _act(t, name) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return MGG_ACT_BF16
-    if t.dtype == torch.float32:
-        return MGG_ACT_F32
-    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    code = _ACTS.get(t.dtype)
+    if code is None:
+        import torch
+        _ACTS.update({torch.bfloat16: MGG_ACT_BF16, torch.float32: MGG_ACT_F32})
+        if t.dtype not in _ACTS:
+            raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+        code = _ACTS[t.dtype]
+    return code
 
 
 def _rows(t, T, H, dtype, name) -> int:
@@ -276,12 +282,8 @@ def _block(x, y, w_after, gate, scale, w_before, alpha, beta, eps):
             kind, ld_gate = MGG_GATE_TOKEN, gate.stride(0) if T > 1 else 1
             _mgg._require(ld_gate >= 1, "gate: values must not overlap")
     param = _param((scale, w_after, w_before), H)
-    return MggBlock(dt, param, T, H, x.data_ptr(), ldx, y.data_ptr(), ldy, kind,
-                    None if gate is None else gate.data_ptr(), ld_gate,
-                    None if scale is None else scale.data_ptr(),
-                    None if w_after is None else w_after.data_ptr(),
-                    None if w_before is None else w_before.data_ptr(), float(alpha),
-                    float(beta), float(eps))
+    return MggBlock(dt, param, T, H, x.data_ptr(), ldx, y.data_ptr(), ldy, kind, _ptr(gate),
+                    ld_gate, _ptr(scale), _ptr(w_after), _ptr(w_before), alpha, beta, eps)
 
 
 def block_norm(x, w, eps=1e-6, u=None):
