@@ -63,7 +63,7 @@ typedef enum { MGG_GATE_NONE = 0, MGG_GATE_TOKEN = 1, MGG_GATE_ELEMENT = 2 } mgg
  *   balance[s] = sum_e (G c_s[e] / (k n_s)) * (sum_{t in s} p[t, e] / n_s),  0 if n_s = 0:
  * 1 when both are even over the experts.
  *
- *   T, G, k     T >= 0; 1 <= G <= 4096; 1 <= k <= min(G, 32).
+ *   T, G, k     0 <= T <= 2^30; 1 <= G <= 4096; 1 <= k <= min(G, 32).
  *   logits      [T] rows of G (ld >= G).      bias  float32 [G] or NULL (sigmoid only).
  *   seq_ends    device int32 [S] or NULL, read by the kernels on every launch; S <= 65535.
  *   scale       finite.
@@ -101,7 +101,7 @@ mgg_status route_topk_backward(mgg_act dt, int T, int G, int k, const void* logi
  *   x_out = alpha * x + beta * scale[c] * g * z               (scale NULL: 1)
  *   u     = rms(x_out; w_before)                              (x_out before its rounding)
  *
- *   T >= 0; 1 <= H <= 32768; eps > 0; alpha, beta finite.
+ *   0 <= T <= 2^30; 1 <= H <= 32768; eps > 0; alpha, beta finite.
  *   x, y        [T] rows of H; gate: [T] values (MGG_GATE_TOKEN, ld_gate the step from one to
  *               the next, >= 1) or [T] rows of H (MGG_GATE_ELEMENT), in the activations' type.
  *   scale, w_after, w_before   [H] of `param`, or NULL.

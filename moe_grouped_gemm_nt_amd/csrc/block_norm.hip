@@ -617,7 +617,7 @@ bool launch(K kernel, int blocks, int threads, size_t lds, const NormArgs& a,
 
 const char* check_block(const NormArgs& a, mgg_act dt, mgg_act param, bool block) {
   if (!known(dt) || !known(param)) return "unknown element type";
-  if (a.T < 0) return "T must not be negative";
+  if (a.T < 0 || a.T > kMaxRows) return "T must be in [0, 2^30]";
   if (a.H < 1 || a.H > kMaxH) return "H must be in [1, 32768]";
   if (!(a.eps > 0.f) || !std::isfinite(a.eps)) return "eps must be positive and finite";
   if (!std::isfinite(a.alpha) || !std::isfinite(a.beta)) return "alpha and beta must be finite";
@@ -747,7 +747,7 @@ mgg_status block_residual_norm(const mgg_block* block, void* x_out, void* u,
 }
 
 size_t block_residual_norm_backward_workspace(int T, int H) {
-  if (T < 0 || H < 1 || H > kMaxH) return 0;
+  if (T < 0 || T > kMaxRows || H < 1 || H > kMaxH) return 0;
   size_t bytes = 0;
   for (int vec : {kVec<bf16_t>, kVec<float>}) {
     const size_t blocks = (size_t)row_blocks(T, threads_backward(H, vec));

@@ -16,6 +16,8 @@ extern "C" void mgg_set_last_error(const char* text) __attribute__((visibility("
 
 namespace mgg_layer {
 
+constexpr int kMaxRows = 1 << 30;  // row numbers plus a grid's worth of rows stay below 2^31
+
 inline mgg_status fail(mgg_status s, const char* text) {
   mgg_set_last_error(text);
   return s;

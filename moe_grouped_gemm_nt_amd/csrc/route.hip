@@ -656,7 +656,7 @@ const char* check_route(mgg_act dt, int T, int G, int k, const void* logits, int
                         mgg_score score, float scale, int S, const int32_t* ends) {
   if (!known(dt)) return "unknown element type";
   if (score != MGG_SCORE_SOFTMAX && score != MGG_SCORE_SIGMOID) return "unknown score function";
-  if (T < 0) return "T must not be negative";
+  if (T < 0 || T > kMaxRows) return "T must be in [0, 2^30]";
   if (G < 1 || G > kMaxExperts) return "G must be in [1, 4096]";
   if (k < 1 || k > G || k > kMaxTopk) return "k must be in [1, min(G, 32)]";
   if (T > 0 && !logits) return "null pointer";
@@ -674,7 +674,7 @@ const char* check_route(mgg_act dt, int T, int G, int k, const void* logits, int
 extern "C" {
 
 size_t route_topk_workspace(int T, int G, int S) {
-  if (T < 0 || G < 1 || G > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
+  if (T < 0 || T > kMaxRows || G < 1 || G > kMaxExperts || S < 1 || S > kMaxSequences) return 0;
   return Workspace(T, G, S).bytes;
 }
 

@@ -304,3 +304,39 @@ def test_offsets_beyond_32_bits():
     gs = mgg.block_residual_norm_backward(dev(s["x"]), dev(s["y"]), dev(s["d_x"]), dev(s["d_x"]), **kw)
     assert torch.equal(g[0][-100:], gs[0]) and torch.equal(g[1][-100:], gs[1])
     assert not g[0][:-100].any() and not g[1][:-100].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H", [64, 250, 256, 1000, 2048, 4100, 7168, 8192])
+def test_many_rows(H, dtype):
+    """Enough rows for workgroups that walk several and keep the parameters in LDS."""
+    say(f"block norm many rows {H} {dtype}")
+    T = 40000 if H <= 256 else 9001 if H <= 2048 else 2100
+    for gate in ("token", "element"):
+        s = make(T, H, dtype, gate)
+        out = check(s, alpha=1.25)
+        # each row is its own: a few of them alone give the same bits
+        kw = {k: dev(v) if torch.is_tensor(v) else v for k, v in params(s, alpha=1.25).items()}
+        rows = slice(T - 3, T)
+        kw["gate"] = kw["gate"][rows]
+        few = mgg.block_residual_norm(dev(s["x"])[rows], dev(s["y"])[rows], **kw)
+        for a, b in zip(few, out):
+            assert (a.double() - b[rows].double()).abs().max() <= \
+                2.0 ** -7 * b[rows].double().abs().max()
+
+
+def test_two_streams():
+    say("block norm streams")
+    ss = [make(3000, 1024, torch.bfloat16, "token"), make(700, 7168, torch.bfloat16, "element")]
+    kws = [{k: dev(v) if torch.is_tensor(v) else v for k, v in params(s).items()} for s in ss]
+    ins = [[dev(s[n]) for n in ("x", "y", "d_x", "d_u")] for s in ss]
+    want = [mgg.block_residual_norm_backward(*i, **k) for i, k in zip(ins, kws)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mgg.block_residual_norm_backward(*ins[i], **kws[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i in range(2) for o in got[i] for a, b in zip(o, want[i]))

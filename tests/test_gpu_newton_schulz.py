@@ -199,3 +199,58 @@ def test_large_wide():
     out = mgg.grouped_newton_schulz(X).double()
     allowed = 4 * (plain - want).norm() / want.norm() + 5 * 2.0 ** -22 * 10.251
     assert (out - want).norm() / want.norm() <= allowed
+
+
+# One shape for every way that a product is dealt: 128-tiles of the symmetric products with the
+# last of them quartered and one full round of 256-tiles; 256-tiles with their last round
+# quartered; 256-tiles of the symmetric products; sides that are no multiple of any tile.
+@pytest.mark.parametrize("G,M,N,dtype", [(4, 2048, 2048, torch.float32),
+                                         (6, 1536, 4096, torch.bfloat16),
+                                         (7, 2048, 2050, torch.float32),
+                                         (5, 3001, 1025, torch.float32)])
+def test_large_shapes(G, M, N, dtype):
+    say(f"ns large {G} {M} {N} {dtype}")
+    g = torch.Generator(device=DEV).manual_seed(M)
+    X = (1e-3 * torch.randn((G, M, N), device=DEV, generator=g)).to(dtype)
+    a, b, c = (float(np.float32(v)) for v in USUAL)
+
+    def steps(m, to):
+        x = (m.double() / (m.double().norm() + 1e-7)).to(to)
+        x = x.t().contiguous() if M > N else x
+        for _ in range(5):
+            A = x @ x.t().contiguous()
+            x = a * x + (b * A + c * (A @ A)) @ x
+        return (x.t() if M > N else x).double()
+
+    out = mgg.grouped_newton_schulz(X)
+    for i in range(G):
+        want, plain = steps(X[i], torch.float64), steps(X[i], torch.float32)
+        allowed = 4 * (plain - want).norm() / want.norm() + 5 * 2.0 ** -22 * 10.251
+        if dtype == torch.bfloat16:
+            allowed += 2.0 ** -8
+        assert (out[i].double() - want).norm() / want.norm() <= allowed, i
+    # captured and replayed, the same bits
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = mgg.grouped_newton_schulz(X)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, out)
+        assert torch.equal(mgg.grouped_newton_schulz(X), out)
+
+
+def test_two_streams():
+    """Calls on two streams at once, each with its own workspace, give the same bits."""
+    say("ns streams")
+    X, Y = momenta(3, 300, 400, torch.float32).to(DEV), momenta(2, 500, 200, torch.bfloat16).to(DEV)
+    want = mgg.grouped_newton_schulz(X), mgg.grouped_newton_schulz(Y)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (s, t) in enumerate(zip(streams, (X, Y))):
+            with torch.cuda.stream(s):
+                got[i].append(mgg.grouped_newton_schulz(t))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for outs, w in zip(got, want) for o in outs)

@@ -319,3 +319,53 @@ def test_offsets_beyond_32_bits():
     off = np.abs(d[-100:].double().cpu().numpy() - want)
     assert (off <= 256 * U * mag + 2.0 ** -8 * np.abs(want)).all()
     assert not d[:-100].any()
+
+
+def test_two_streams():
+    """Calls on two streams at once give the same bits as one after the other."""
+    say("route streams")
+    ls = [logits_of(5000, 288, torch.float32, 70).to(DEV), logits_of(3000, 40, torch.bfloat16, 71).to(DEV)]
+    want = [mgg.route_topk(l, 8) for l in ls]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(mgg.route_topk(ls[i], 8))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i in range(2) for o in got[i] for a, b in zip(o, want[i]))
+
+
+@pytest.mark.parametrize("G", [16, 60, 64, 100, 128, 160, 192, 250, 256, 272, 288, 300, 320])
+def test_crowded_candidates(G):
+    """Rows whose candidates do not fit the ranking (few distinct values) next to rows whose
+    candidates do: each row's result is the definition's, and the same beside other rows."""
+    say(f"route crowded {G}")
+    l = logits_of(64, G, torch.float32, 80 + G)
+    l[::3] = torch.round(l[::3])
+    l[1::3] = torch.where(l[1::3] > 0, 1.0, l[1::3])
+    for k in (1, min(G, 8), min(G, 17), min(G, 32)):
+        ids, w = check_forward(l, k)[:2]
+        for t in (0, 1, 2, 31, 63):
+            i1, w1 = mgg.route_topk(l[t:t + 1].to(DEV), k, balance=False)
+            assert torch.equal(i1[0], ids[t]) and torch.equal(w1[0], w[t])
+        b = torch.round(4 * torch.randn(G, generator=torch.Generator().manual_seed(G))) / 8
+        check_forward(l, k, bias=b, score="sigmoid")
+
+
+def test_bias_of_any_size():
+    """Biases from forbidding to forcing an expert, and large ones that swallow the scores."""
+    say("route bias sizes")
+    l = logits_of(48, 96, torch.float32, 90)
+    b = 0.1 * torch.randn(96, generator=torch.Generator().manual_seed(4))
+    for value in (float("-inf"), -1e6, 1e6, 3e38):
+        b[7], b[50] = value, value
+        ids = check_forward(l, 8, bias=b, score="sigmoid")[0]
+        assert ((ids[:, :2] == torch.tensor([7, 50], device=DEV, dtype=torch.int32)).all()
+                if value > 0 and value != 1e6 else True)
+    b[:] = 1e4 + 0.5 * torch.arange(96) % 3
+    check_forward(l, 8, bias=b, score="sigmoid")
+    b[7] = float("inf")
+    ids, w = mgg.route_topk(l.to(DEV), 8, bias=b.to(DEV), score="sigmoid", balance=False)
+    assert (ids[:, 0] == 7).all() and torch.isfinite(w).all()
