@@ -62,9 +62,12 @@ __device__ __forceinline__ float exp_neg(float x) {
   return __builtin_amdgcn_exp2f(x * 1.44269504f);
 }
 
+// 1 / x to within one unit in the last place, for x in a float's normal range.
+__device__ __forceinline__ float reciprocal(float x) { return __builtin_amdgcn_rcpf(x); }
+
 // sigmoid(v) and 1 - sigmoid(v), each to the relative precision of exp_neg.
 __device__ __forceinline__ void sigmoid_parts(float v, float& q, float& one_minus_q) {
-  const float a = exp_neg(-fabsf(v)), r = 1.f / (1.f + a);
+  const float a = exp_neg(-fabsf(v)), r = reciprocal(1.f + a);
   q = v >= 0.f ? r : a * r;
   one_minus_q = v >= 0.f ? a * r : r;
 }

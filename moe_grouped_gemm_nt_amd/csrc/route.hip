@@ -25,9 +25,10 @@ constexpr int kThreads = 256;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxExperts = 4096;
 constexpr int kMaxSequences = 65535;  // grid.y of the summing kernel
-// Most workgroups that rows are dealt to: four for each CU. Selection with a bias has registers
-// for two or three on a CU and takes two.
-constexpr int kRowBlocks = 1024, kRowBlocksBias = 512;
+// Most workgroups that rows are dealt to, for each of the 256 CUs: four, or two where a workgroup
+// has a start and an end to pay for (counts and sums: below kLongChunk rows each) or the
+// registers allow no more (selection with a bias).
+constexpr int kRowBlocks = 1024, kRowBlocksFew = 512, kLongChunk = 64;
 
 struct RouteArgs {
   const void* logits;
@@ -60,13 +61,30 @@ struct Scores {
   __device__ __forceinline__ float hat(float l) const {
     if constexpr (!SIGMOID) return exp_neg(l - m);
     const float a = exp_neg(-fabsf(l));
-    const float num = m < 0.f ? exp_neg(l - m) : (l < 0.f ? a : 1.f);
-    return num / (1.f + a);
+    return (m < 0.f ? exp_neg(l - m) : (l < 0.f ? a : 1.f)) * reciprocal(1.f + a);
+  }
+  // of a whole row: the shifted exponentials only where the row has no logit above 0
+  template <int V>
+  __device__ __forceinline__ void hats(const float (&l)[V], float (&h)[V]) const {
+    if constexpr (!SIGMOID) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = exp_neg(l[v] - m);
+    } else if (m < 0.f) {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        h[v] = exp_neg(l[v] - m) * reciprocal(1.f + exp_neg(-fabsf(l[v])));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float a = exp_neg(-fabsf(l[v]));
+        h[v] = (l[v] < 0.f ? a : 1.f) * reciprocal(1.f + a);
+      }
+    }
   }
   // 1 - sigmoid(l)
   __device__ __forceinline__ static float one_minus_q(float l) {
     const float a = exp_neg(-fabsf(l));
-    return (l >= 0.f ? a : 1.f) / (1.f + a);
+    return (l >= 0.f ? a : 1.f) * reciprocal(1.f + a);
   }
 };
 
@@ -147,8 +165,9 @@ __device__ __forceinline__ KeyOf<BIAS> key_of(float l, const float* bias, int e)
 
 // The k first experts by key, one after another: every round takes the largest key that is left
 // (the lower index among equals; never NaN or -inf). For any row, at about 5 k V operations.
-template <int L, int V, bool BIAS, class Hat>
-__device__ __forceinline__ Chosen<L> choose_by_rounds(const RouteArgs& a, int lane,
+// With a bias it goes over the row in memory: its float64 keys would cost every row registers.
+template <class T, int L, int V, bool BIAS, class Hat>
+__device__ __forceinline__ Chosen<L> choose_by_rounds(const RouteArgs& a, const T* row, int lane,
                                                       const float (&l)[V], Hat hat_of) {
   using Key = KeyOf<BIAS>;
   uint64_t taken = 0;  // slots
@@ -159,13 +178,19 @@ __device__ __forceinline__ Chosen<L> choose_by_rounds(const RouteArgs& a, int la
     Key best = -INFINITY;
     int e = INT32_MAX;
     float logit = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
+    auto see = [&](int v, float value) {
       const int at = lane + L * v;
-      if (at < a.G && l[v] > -INFINITY && !(taken >> v & 1)) {
-        const Key key = key_of<BIAS>(l[v], a.bias, at);
-        if (key > best) best = key, e = at, logit = l[v];
+      if (value > -INFINITY && !(taken >> v & 1)) {
+        const Key key = key_of<BIAS>(value, a.bias, at);
+        if (key > best) best = key, e = at, logit = value;
       }
+    };
+    if constexpr (BIAS) {
+#pragma unroll 1
+      for (int v = 0; lane + L * v < a.G; ++v) see(v, to_f32(row[lane + L * v]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) see(v, l[v]);
     }
     const Key top = lanes_reduce<L>(best, [](Key x, Key y) { return x > y ? x : y; });
     const int first = lanes_reduce<L>(best == top ? e : INT32_MAX,
@@ -196,16 +221,17 @@ __device__ __forceinline__ uint64_t order_of(float key, int e) {
 template <class T, int L, int V, bool SIGMOID, bool BIAS, class Hat>
 __device__ __forceinline__ bool choose_by_candidates(const RouteArgs& a, const T* row, int lane,
                                                      const float (&l)[V], const float (&hat)[V],
-                                                     float to_q, Hat hat_of, int* s_id,
-                                                     uint64_t* s_order, Chosen<L>& c) {
-  auto rough = [&](int v) {  // what the bound is taken on
-    if constexpr (!BIAS) return l[v];
-    const int e = lane + L * v;
-    return e < a.G && l[v] > -INFINITY ? hat[v] * to_q + a.bias[e] : -INFINITY;
-  };
+                                                     const float* bias, float to_q, Hat hat_of,
+                                                     int* s_id, uint64_t* s_order,
+                                                     Chosen<L>& c) {
+  float rough[V];  // what the bound is taken on
   float most = -INFINITY;
 #pragma unroll
-  for (int v = 0; v < V; ++v) most = fmaxf(most, rough(v));
+  for (int v = 0; v < V; ++v) {
+    if constexpr (BIAS) rough[v] = l[v] > -INFINITY ? fmaf(hat[v], to_q, bias[v]) : -INFINITY;
+    else rough[v] = l[v];
+    most = fmaxf(most, rough[v]);
+  }
   // lanes apart by their number in the last bits: k rounds take k lanes
   uint32_t left = (ordered(most) & ~(uint32_t)(L - 1)) | (uint32_t)lane, bound = 0;
   for (int r = 0; r < a.k; ++r) {
@@ -219,7 +245,7 @@ __device__ __forceinline__ bool choose_by_candidates(const RouteArgs& a, const T
   using Bits = std::conditional_t<(V > 32), uint64_t, uint32_t>;
   Bits slots = 0;
 #pragma unroll
-  for (int v = 0; v < V; ++v) slots |= rough(v) >= least ? (Bits)1 << v : 0;
+  for (int v = V - 1; v >= 0; --v) slots = slots + slots + (rough[v] >= least ? 1 : 0);
   const int mine = V > 32 ? __popcll(slots) : __popc((uint32_t)slots);
   const int upto = lanes_prefix<L>(mine);
   const int total = __shfl(upto, L - 1, L);
@@ -273,16 +299,14 @@ __device__ __forceinline__ bool choose_by_candidates(const RouteArgs& a, const T
 template <class T, class SHAPE, bool SIGMOID, bool BIAS, bool STATS>
 __device__ __forceinline__ void route_row(const RouteArgs& a, const T* row, int t, bool active,
                                           int lane, const float (&l)[SHAPE::V],
-                                          float (&acc)[SHAPE::V], int* s_count, int* s_id,
-                                          uint64_t* s_order) {
+                                          const float* bias, float (&acc)[SHAPE::V],
+                                          int* s_count, int* s_id, uint64_t* s_order) {
   constexpr int L = SHAPE::L, V = SHAPE::V;
   const Scores<SIGMOID> sc(row_max<L>(l));
   float hat[V], sum = 0.f;
+  sc.hats(l, hat);
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    hat[v] = sc.hat(l[v]);
-    sum += hat[v];
-  }
+  for (int v = 0; v < V; ++v) sum += hat[v];
   sum = lanes_sum<L>(sum);
   const float inv_sum = sum == 0.f ? 0.f : 1.f / sum;
   if constexpr (STATS) {
@@ -293,9 +317,9 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, const T* row, int 
   }
   auto hat_of = [&](float logit) { return sc.hat(logit); };
   Chosen<L> c;
-  if (!choose_by_candidates<T, L, V, SIGMOID, BIAS>(a, row, lane, l, hat, sc.to_q, hat_of, s_id,
-                                                    s_order, c))
-    c = choose_by_rounds<L, V, BIAS>(a, lane, l, hat_of);
+  if (!choose_by_candidates<T, L, V, SIGMOID, BIAS>(a, row, lane, l, hat, bias, sc.to_q, hat_of,
+                                                    s_id, s_order, c))
+    c = choose_by_rounds<T, L, V, BIAS>(a, row, lane, l, hat_of);
   float chosen = 0.f;
 #pragma unroll
   for (int i = 0; i < c.N; ++i) chosen += c.rank[i] < a.k ? c.hat[i] : 0.f;
@@ -328,6 +352,9 @@ __global__ __launch_bounds__(kThreads) void route_rows(RouteArgs a) {
     if (blockIdx.x == 0)
       for (int s = threadIdx.x; s < a.S; s += kThreads) a.counters[s] = 0;
 
+  float bias[BIAS ? V : 1];  // -inf past the row, so that nothing is taken there
+  if constexpr (BIAS) load_row<SHAPE>(a.bias, a.G, lane, bias);
+
   int row = r0, s = -1;
   while (row < r1) {
     int end = r1;
@@ -353,8 +380,8 @@ __global__ __launch_bounds__(kThreads) void route_rows(RouteArgs a) {
       const int t = base + grp;
       float l[V];
       load_row<SHAPE>(row_at(t), a.G, lane, l);
-      route_row<T, SHAPE, SIGMOID, BIAS, STATS>(a, row_at(t), t, t < end, lane, l, acc, s_count,
-                                                s_id[grp], s_order[grp]);
+      route_row<T, SHAPE, SIGMOID, BIAS, STATS>(a, row_at(t), t, t < end, lane, l, bias, acc,
+                                                s_count, s_id[grp], s_order[grp]);
     }
     if constexpr (STATS) {
       // the sums of a wave's rows, then those of the waves one after another
@@ -576,9 +603,9 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
       }
       const Scores<SIGMOID> sc(row_max<L>(l));
       float sum = 0.f, q_sum = 0.f, q_dw = 0.f;
+      sc.hats(l, h);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        h[v] = sc.hat(l[v]);
         sum += h[v];
         q_sum += chosen >> v & 1 ? h[v] : 0.f;
         q_dw += chosen >> v & 1 ? h[v] * g[v] : 0.f;
@@ -696,7 +723,8 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
     return fail(MGG_EINVAL, "counts, tokens and balance are given together");
   if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(balance, 4))
     return fail(MGG_EINVAL, "counts, tokens and balance must be 4-byte aligned");
-  const int rows = rows_per_block(T, G, bias ? kRowBlocksBias : kRowBlocks);
+  const bool few = bias || (stats && T < kRowBlocks * kLongChunk);
+  const int rows = rows_per_block(T, G, few ? kRowBlocksFew : kRowBlocks);
   RouteArgs a{logits, ld,       bias, T,       G,    k,       S,       renormalize,
               scale,  seq_ends, ids,  weights, rows, nullptr, nullptr, nullptr};
   double* dots = nullptr;
