@@ -79,23 +79,51 @@ struct NsArgs {
   int norm_blocks;
 };
 
+// Eight elements of the caller's matrix from `p`, which is aligned to an element only; `n` of them
+// exist.
+__device__ __forceinline__ void load_eight(const void* in, int bf16, size_t at, long n,
+                                           float (&v)[8]) {
+  if (bf16) {
+    const bf16_t* p = reinterpret_cast<const bf16_t*>(in) + at;
+    uint16_t bits[8];
+    if (n >= 8) {
+      __builtin_memcpy(bits, p, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) bits[i] = i < n ? p[i].bits : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32(bf16_t{bits[i]});
+  } else {
+    const float* p = reinterpret_cast<const float*>(in) + at;
+    if (n >= 8) {
+      __builtin_memcpy(v, p, 32);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.f;
+    }
+  }
+}
+
 // Sums of squares in float64: a float32 overflows above 1e19.
 __global__ __launch_bounds__(kThreads) void ns_norm(NsArgs a) {
   __shared__ double s_sum[kThreads / 64];
   const size_t size = (size_t)a.M * a.N, base = size * blockIdx.y;
   double sum = 0.0;
-  constexpr int AT_ONCE = 16;
-  for (size_t i0 = (size_t)blockIdx.x * kThreads * AT_ONCE; i0 < size;
-       i0 += (size_t)gridDim.x * kThreads * AT_ONCE) {
-    float v[AT_ONCE];
+  constexpr int AT_ONCE = 2;
+  const size_t step = (size_t)gridDim.x * kThreads * 8;
+  for (size_t i0 = ((size_t)blockIdx.x * kThreads + threadIdx.x) * 8; i0 < size;
+       i0 += AT_ONCE * step) {
+    float v[AT_ONCE][8];
 #pragma unroll
     for (int u = 0; u < AT_ONCE; ++u) {
-      const size_t i = i0 + u * kThreads + threadIdx.x;
-      v[u] = i >= size ? 0.f : a.in_bf16 ? to_f32(reinterpret_cast<const bf16_t*>(a.in)[base + i])
-                                         : reinterpret_cast<const float*>(a.in)[base + i];
+      const size_t i = i0 + u * step;
+      load_eight(a.in, a.in_bf16, base + (i < size ? i : 0), i < size ? (long)(size - i) : 0, v[u]);
     }
 #pragma unroll
-    for (int u = 0; u < AT_ONCE; ++u) sum += (double)v[u] * (double)v[u];
+    for (int u = 0; u < AT_ONCE; ++u)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += (double)v[u][e] * (double)v[u][e];
   }
   sum = lanes_sum<64>(sum);
   if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = sum;
@@ -108,8 +136,24 @@ __global__ __launch_bounds__(kThreads) void ns_norm(NsArgs a) {
 
 constexpr int kSplitTile = 64;
 
-// Scales a matrix to norm 1 and writes X and X^T in halves, padded with zeros.
+// Eight values as eight hi and eight lo.
+__device__ __forceinline__ void store_eight(const Split& to, size_t at, const float (&v)[8]) {
+  v8h hi, lo;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    _Float16 h, l;
+    split(v[i], h, l);
+    hi[i] = h;
+    lo[i] = l;
+  }
+  *reinterpret_cast<v8h*>(to.hi + at) = hi;
+  *reinterpret_cast<v8h*>(to.lo + at) = lo;
+}
+
+// Scales a matrix to norm 1 and writes X and X^T in halves, padded with zeros: 64 x 64 values a
+// workgroup, eight of a row (then of a column, by way of LDS) a thread.
 __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt) {
+  // rows 65 words apart: the columns' readers meet different banks
   __shared__ float s_tile[kSplitTile][kSplitTile + 1];
   // every wave adds the partial sums in the same order
   double sum = 0.0;
@@ -117,35 +161,32 @@ __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt
     sum += a.norms[(size_t)blockIdx.z * kNormBlocks + i];
   sum = lanes_sum<64>(sum);
   const double inv = (double)kScaleX / (sqrt(sum) + (double)a.eps);
-  // the caller's rows run along tile rows here
-  const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
-  const int col = threadIdx.x % kSplitTile, row = threadIdx.x / kSplitTile;
-  const size_t base = (size_t)a.M * a.N * blockIdx.z;
-  // in the caller's orientation, `direct` has the input's rows as rows
+  // the caller's rows run along tile rows here; `direct` has them as rows
   const Split direct = a.tall ? xt : x, turned = a.tall ? x : xt;
-  for (int r = row; r < kSplitTile; r += kThreads / kSplitTile) {
-    const int i = r0 + r, j = c0 + col;
-    float v = 0.f;
-    if (i < a.M && j < a.N) {
-      const size_t at = base + (size_t)i * a.N + j;
-      v = a.in_bf16 ? to_f32(reinterpret_cast<const bf16_t*>(a.in)[at])
-                    : reinterpret_cast<const float*>(a.in)[at];
-      v = (float)((double)v * inv);
+  const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
+  const size_t base = (size_t)a.M * a.N * blockIdx.z;
+#pragma unroll
+  for (int q = 0; q < kSplitTile * kSplitTile / (8 * kThreads); ++q) {
+    const int at = q * kThreads + threadIdx.x, r = at / (kSplitTile / 8), c = at % (kSplitTile / 8) * 8;
+    const int i = r0 + r, j = c0 + c;
+    const bool in = i < a.M && j < a.N;
+    float v[8];
+    load_eight(a.in, a.in_bf16, in ? base + (size_t)i * a.N + j : 0, in ? a.N - j : 0, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = (float)((double)v[e] * inv);
+      s_tile[r][c + e] = v[e];
     }
-    s_tile[r][col] = v;
-    _Float16 hi, lo;
-    split(v, hi, lo);
-    const size_t to = direct.at(blockIdx.z, i, j);
-    direct.hi[to] = hi;
-    direct.lo[to] = lo;
+    store_eight(direct, direct.at(blockIdx.z, i, j), v);
   }
   __syncthreads();
-  for (int r = row; r < kSplitTile; r += kThreads / kSplitTile) {
-    _Float16 hi, lo;
-    split(s_tile[col][r], hi, lo);
-    const size_t to = turned.at(blockIdx.z, c0 + r, r0 + col);
-    turned.hi[to] = hi;
-    turned.lo[to] = lo;
+#pragma unroll
+  for (int q = 0; q < kSplitTile * kSplitTile / (8 * kThreads); ++q) {
+    const int at = q * kThreads + threadIdx.x, c = at % kSplitTile, r = at / kSplitTile * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = s_tile[r + e][c];
+    store_eight(turned, turned.at(blockIdx.z, c0 + c, r0 + r), v);
   }
 }
 
