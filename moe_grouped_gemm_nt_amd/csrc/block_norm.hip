@@ -175,7 +175,8 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* s, int& turn) {
   }
 }
 
-constexpr int block_threads(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Workgroups hold several rows of a wave or less, or one row.
+constexpr int block_threads(int tpr) { return tpr <= 64 ? 256 : tpr; }
 
 // The thread's row group in its workgroup: the same for a whole wave from 64 threads a row on.
 template <int TPR>
@@ -194,13 +195,15 @@ struct Columns {
   const float* lds;
   int Hp;
   __device__ __forceinline__ void stage(float* to) const {
-    for (int c = threadIdx.x; c < Hp; c += blockDim.x) {
-      float wa[1], sc[1], wb[1];
-      load_param(a.w_after, a.param_bf16, c, a.H, 1.f, wa);
-      load_param(a.scale, a.param_bf16, c, a.H, 1.f, sc);
-      load_param(a.w_before, a.param_bf16, c, a.H, 1.f, wb);
-      to[c] = wa[0] * sc[0];
-      to[Hp + c] = wb[0];
+    for (int c = threadIdx.x * VEC; c < Hp; c += blockDim.x * VEC) {
+      float wa[VEC], sc[VEC], wb[VEC];
+      from_memory(a.w_after, c, wa);
+      from_memory(a.scale, c, sc);
+      from_memory(a.w_before, c, wb);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) wa[i] *= sc[i];
+      __builtin_memcpy(__builtin_assume_aligned(to + c, 16), wa, VEC * 4);
+      __builtin_memcpy(__builtin_assume_aligned(to + Hp + c, 16), wb, VEC * 4);
     }
     __syncthreads();
   }
@@ -208,7 +211,10 @@ struct Columns {
     if constexpr (WHOLE) load_param_whole(p, a.param_bf16, c, a.H, 1.f, v);
     else load_param(p, a.param_bf16, c, a.H, 1.f, v);
   }
+  // Read anew for every row: kept in registers over the rows they cost more in occupancy (and, with
+  // a gate per element, spills) than they save.
   __device__ __forceinline__ void from_lds(int c, float (&v)[VEC]) const {
+    asm volatile("" ::: "memory");
     __builtin_memcpy(v, __builtin_assume_aligned(lds + c, 16), VEC * 4);
   }
   // for VEC columns from `c`; columns past the row give anything finite
@@ -561,11 +567,11 @@ int threads_backward(int H, int vec) {
 int resident_groups(int tpr) { return 256 * 1024 / tpr; }
 
 // Workgroups of the backward kernel, each with its own column sums: one round of resident ones,
-// with at least four rows for each of a workgroup's groups where there are as many, so that the
+// with at least two rows for each of a workgroup's groups where there are as many, so that the
 // sums' traffic stays small next to the rows'.
 int row_blocks(int T, int tpr) {
   const int per = block_threads(tpr) / tpr;
-  const int rows = std::max(4, cdiv(T, resident_groups(tpr)));
+  const int rows = std::max(2, cdiv(T, resident_groups(tpr)));
   return std::max(1, cdiv(T, rows * per));
 }
 
