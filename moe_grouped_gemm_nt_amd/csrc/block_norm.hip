@@ -121,37 +121,31 @@ __device__ __forceinline__ void store_piece(T* row, int c, int H, const float (&
   }
 }
 
-// VEC values of a parameter vector from column `c`; `missing` where there is no vector, anything
-// finite past the row.
+// VEC values of a parameter vector of H from column `c`; `missing` where there is no vector, anything
+// finite past its end.
 template <int VEC>
 __device__ __forceinline__ void load_param(const void* p, int bf16, int c, int H, float missing,
                                            float (&v)[VEC]) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) v[i] = missing;
   if (p == nullptr) return;
+  const char* base = reinterpret_cast<const char*>(p);
+  if (c + VEC <= H) {
+    if (bf16) {
+      uint16_t bits[VEC];
+      __builtin_memcpy(bits, base + (uint32_t)c * 2u, VEC * 2);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = to_f32(bf16_t{bits[i]});
+    } else {
+      __builtin_memcpy(v, base + (uint32_t)c * 4u, VEC * 4);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < VEC; ++i) {
     const uint32_t at = (uint32_t)min(c + i, H - 1);
     v[i] = bf16 ? to_f32(reinterpret_cast<const bf16_t*>(p)[at])
                 : reinterpret_cast<const float*>(p)[at];
-  }
-}
-
-// The same for a float32 or bf16 vector whose length is a multiple of VEC.
-template <int VEC>
-__device__ __forceinline__ void load_param_whole(const void* p, int bf16, int c, int H,
-                                                 float missing, float (&v)[VEC]) {
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) v[i] = missing;
-  if (p == nullptr || c >= H) return;
-  const char* base = reinterpret_cast<const char*>(p);
-  if (bf16) {
-    uint16_t bits[VEC];
-    __builtin_memcpy(bits, base + (uint32_t)c * 2u, VEC * 2);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = to_f32(bf16_t{bits[i]});
-  } else {
-    __builtin_memcpy(v, base + (uint32_t)c * 4u, VEC * 4);
   }
 }
 
@@ -208,8 +202,7 @@ struct Columns {
     __syncthreads();
   }
   __device__ __forceinline__ void from_memory(const void* p, int c, float (&v)[VEC]) const {
-    if constexpr (WHOLE) load_param_whole(p, a.param_bf16, c, a.H, 1.f, v);
-    else load_param(p, a.param_bf16, c, a.H, 1.f, v);
+    load_param(p, a.param_bf16, c, a.H, 1.f, v);
   }
   // Read anew for every row: kept in registers over the rows they cost more in occupancy (and, with
   // a gate per element, spills) than they save.
