@@ -51,8 +51,9 @@ struct Piece {
 
 // The piece at column `c` of a row of H. Rows are the wave's (a scalar address), columns the
 // lane's (a 32-bit offset to it). WHOLE: H is a multiple of the piece. Otherwise the last piece
-// is read so that it ends with the row, and shifted down; rows shorter than a piece go by
-// elements.
+// is read so that it ends with the row, and settle() shifts it into place - later, where the
+// piece is used: the wave that holds it would otherwise wait here for each of its loads. Rows
+// shorter than a piece go by elements.
 template <bool WHOLE, class T>
 __device__ __forceinline__ Piece<T> load_piece(const T* row, int c, int H) {
   constexpr int VEC = kVec<T>;
@@ -62,14 +63,6 @@ __device__ __forceinline__ Piece<T> load_piece(const T* row, int c, int H) {
   if (WHOLE || H >= VEC) {
     const int from = WHOLE ? c : min(c, H - VEC);
     __builtin_memcpy(&r, base + (uint32_t)from * (uint32_t)sizeof(T), 16);
-    if (!WHOLE && from < c) {
-      uint32_t by = (uint32_t)(c - from) * (uint32_t)sizeof(T) * 8;  // bits, below 128
-      if (by & 64) r = Piece<T>{{r.w[2], r.w[3], 0u, 0u}};
-      if (by & 32) r = Piece<T>{{r.w[1], r.w[2], r.w[3], 0u}};
-      if (by & 16)
-        r = Piece<T>{{r.w[0] >> 16 | r.w[1] << 16, r.w[1] >> 16 | r.w[2] << 16,
-                      r.w[2] >> 16 | r.w[3] << 16, r.w[3] >> 16}};
-    }
   } else {
     uint64_t half[2] = {0, 0};
 #pragma unroll 1
@@ -83,6 +76,18 @@ __device__ __forceinline__ Piece<T> load_piece(const T* row, int c, int H) {
     __builtin_memcpy(&r, half, 16);
   }
   return r;
+}
+template <bool WHOLE, class T>
+__device__ __forceinline__ void settle(Piece<T>& r, int c, int H) {
+  if constexpr (!WHOLE) {
+    if (H < kVec<T> || c >= H || c + kVec<T> <= H) return;
+    const uint32_t by = (uint32_t)(c + kVec<T> - H) * (uint32_t)sizeof(T) * 8;  // bits, below 128
+    if (by & 64) r = Piece<T>{{r.w[2], r.w[3], 0u, 0u}};
+    if (by & 32) r = Piece<T>{{r.w[1], r.w[2], r.w[3], 0u}};
+    if (by & 16)
+      r = Piece<T>{{r.w[0] >> 16 | r.w[1] << 16, r.w[1] >> 16 | r.w[2] << 16,
+                    r.w[2] >> 16 | r.w[3] << 16, r.w[3] >> 16}};
+  }
 }
 
 template <bool WHOLE, class T>
@@ -264,8 +269,14 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_forward(NormArgs a) {
   if (t >= a.T) return;  // whole waves, and whole workgroups where a barrier follows
   Row next = load(t);
   for (; t < a.T; t += stride) {
-    const Row in = next;
+    Row in = next;
     if (t + stride < a.T) next = load(t + stride);
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int col = (c * TPR + tid) * VEC;
+      if constexpr (BLOCK) settle<WHOLE>(in.y[c], col, H);
+      settle<WHOLE>(in.x[c], col, H);
+    }
     float out[NV][VEC];
     if constexpr (BLOCK) {
       const T* gr = row_of<T>(a.gate, a.ld_gate, t);
@@ -291,7 +302,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_forward(NormArgs a) {
         float w[VEC];
         columns.block(col, w);
         Piece<T> gs;
-        if (a.gate_kind == MGG_GATE_ELEMENT) gs = load_piece<WHOLE>(gr, col, H);
+        if (a.gate_kind == MGG_GATE_ELEMENT) {
+          gs = load_piece<WHOLE>(gr, col, H);
+          settle<WHOLE>(gs, col, H);
+        }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           float g = row * w[i];
@@ -389,6 +403,16 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_backward(NormArgs a) 
     } else {
       in = load(t);
     }
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const int col = (c * TPR + tid) * VEC;
+      if (before) {
+        settle<WHOLE>(in.x[c], col, H);
+        settle<WHOLE>(in.du[c], col, H);
+      }
+      if constexpr (BLOCK != 0) settle<WHOLE>(in.y[c], col, H);
+      settle<WHOLE>(in.dx[c], col, H);
+    }
     const Piece<T>(&xs)[NV] = in.x, (&ys)[NV] = in.y, (&dxs)[NV] = in.dx, (&dus)[NV] = in.du;
     const T* gr = row_of<T>(a.gate, a.ld_gate, t);
     float sums[3] = {0.f, 0.f, 0.f};  // x x, du w_before x, y y
@@ -441,7 +465,10 @@ __global__ __launch_bounds__(block_threads(TPR)) void norm_backward(NormArgs a) 
         float w[VEC], dg[VEC];
         columns.block(col, w);
         Piece<T> gs;
-        if constexpr (ELEMENT) gs = load_piece<WHOLE>(gr, col, H);
+        if constexpr (ELEMENT) {
+          gs = load_piece<WHOLE>(gr, col, H);
+          settle<WHOLE>(gs, col, H);
+        }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
           if constexpr (ELEMENT) sigmoid_parts(gs.at(i), gate, not_gate);
