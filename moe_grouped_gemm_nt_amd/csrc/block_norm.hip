@@ -127,15 +127,15 @@ __device__ __forceinline__ void store_piece(T* row, int c, int H, const float (&
 }
 
 // VEC values of a parameter vector of H from column `c`; `missing` where there is no vector, anything
-// finite past its end.
-template <int VEC>
+// finite past its end. WHOLE: H and c are multiples of VEC.
+template <bool WHOLE, int VEC>
 __device__ __forceinline__ void load_param(const void* p, int bf16, int c, int H, float missing,
                                            float (&v)[VEC]) {
 #pragma unroll
   for (int i = 0; i < VEC; ++i) v[i] = missing;
-  if (p == nullptr) return;
+  if (p == nullptr || (WHOLE && c >= H)) return;
   const char* base = reinterpret_cast<const char*>(p);
-  if (c + VEC <= H) {
+  if (WHOLE || c + VEC <= H) {
     if (bf16) {
       uint16_t bits[VEC];
       __builtin_memcpy(bits, base + (uint32_t)c * 2u, VEC * 2);
@@ -207,7 +207,7 @@ struct Columns {
     __syncthreads();
   }
   __device__ __forceinline__ void from_memory(const void* p, int c, float (&v)[VEC]) const {
-    load_param(p, a.param_bf16, c, a.H, 1.f, v);
+    load_param<WHOLE>(p, a.param_bf16, c, a.H, 1.f, v);
   }
   // Read anew for every row: kept in registers over the rows they cost more in occupancy (and, with
   // a gate per element, spills) than they save.
@@ -564,8 +564,8 @@ __global__ __launch_bounds__(kSumCols* kSumStrips) void norm_column_sums(
     return;
   }
   float sc[1], wa[1];
-  load_param(a.scale, a.param_bf16, c, a.H, 1.f, sc);
-  load_param(a.w_after, a.param_bf16, c, a.H, 1.f, wa);
+  load_param<false>(a.scale, a.param_bf16, c, a.H, 1.f, sc);
+  load_param<false>(a.w_after, a.param_bf16, c, a.H, 1.f, wa);
   if (d_scale != nullptr) d_scale[c] = (float)(sum * (double)a.beta * (double)wa[0]);
   if (d_w_after != nullptr) d_w_after[c] = (float)(sum * (double)a.beta * (double)sc[0]);
 }
