@@ -197,6 +197,10 @@ struct ProductArgs {
   int K;
   int tiles_i, tiles_j;  // of one matrix
   int whole;             // tiles of all matrices that are not cut into quarters
+  // kGram: the parts that a tile's sum is cut into, of part_k elements of K (the last one may be
+  // shorter), and where their sums go; one part: straight on to the result
+  int part_k, parts;
+  float* sums;
   float to_value;     // accumulator -> value: the operands' powers of two taken back
   Split c, ct;        // the result and its transpose (symmetric results: the same matrix)
   // kPoly: P = ca I + cb A + cc A A
@@ -286,9 +290,9 @@ __device__ __forceinline__ void store_out(const uint32_t* words, int ld_words, c
 // library product of 8192 x 8192 fp16 matrices reaches 1110 there), with the matrix pipe busy
 // 67 % of the cycles at the 1.7 GHz that the power limit leaves; A and P take 105-115 us.
 template <Product WHAT, class TILE>
-__device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_lds, size_t g,
-                                             int i0, int j0) {
-  constexpr bool SYM = WHAT == kGram || WHAT == kPoly;
+__device__ __forceinline__ void tile_sum(const ProductArgs& p, uint8_t* s_lds, size_t g, int i0,
+                                         int j0, int k0, int k_len,
+                                         v16f (&acc)[TILE::RI][TILE::RJ]) {
   constexpr int RI = TILE::RI, RJ = TILE::RJ;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -304,6 +308,7 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_ld
     const Split& op = h < 2 ? p.left : p.right;
     const _Float16* half = (h & 1) ? op.lo : op.hi;
     from[q] = reinterpret_cast<const uint8_t*>(half + g * op.group +
+                                               (size_t)k0 * op.rows +
                                                (size_t)(h < 2 ? i0 : j0) * kSlice) +
               at % TILE::HALF;
     further[q] = op.rows * kSlice * 2;
@@ -314,7 +319,6 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_ld
     from[q] += further[q];
   };
 
-  v16f acc[RI][RJ];
 #pragma unroll
   for (int i = 0; i < RI; ++i)
 #pragma unroll
@@ -367,7 +371,7 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_ld
   // s + 1, so step s + 1 may read the one and step s + 2 copy over the other. While copies go
   // on, those of the S - 3 slices behind s + 2 may still be under way.
   constexpr int S = TILE::S, AHEAD = S - 1;
-  const int slices = p.K / kSlice;  // a multiple of four
+  const int slices = k_len / kSlice;  // a multiple of four
   Step even, odd;
   for (int s = 0; s < AHEAD && s < slices; ++s)
 #pragma unroll
@@ -402,7 +406,18 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_ld
   } else {
     steps(integral_constant<int, 12>{}, integral_constant<int, AHEAD>{});
   }
-  // the stages become the waves' turning space
+}
+
+// Writes a tile's sums, in the caller's or the next product's form.
+template <Product WHAT, class TILE>
+__device__ __forceinline__ void tile_write(const ProductArgs& p, uint8_t* s_lds, size_t g, int i0,
+                                           int j0, v16f (&acc)[TILE::RI][TILE::RJ]) {
+  constexpr bool SYM = WHAT == kGram || WHAT == kPoly;
+  constexpr int RI = TILE::RI, RJ = TILE::RJ;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / TILE::WJ * 32 * RI, wj = wave % TILE::WJ * 32 * RJ;
+  // LDS, whose stages everyone has read, is the waves' turning space
 
   // lane: row 32 i + (lane & 31) of the wave's part; registers 4 q .. 4 q + 3: columns
   // 32 j + 8 q + 4 (lane >> 5) ..
@@ -463,6 +478,73 @@ __device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_ld
     }
 }
 
+template <Product WHAT, class TILE>
+__device__ __forceinline__ void tile_product(const ProductArgs& p, uint8_t* s_lds, size_t g,
+                                             int i0, int j0) {
+  v16f acc[TILE::RI][TILE::RJ];
+  tile_sum<WHAT, TILE>(p, s_lds, g, i0, j0, 0, p.K, acc);
+  tile_write<WHAT, TILE>(p, s_lds, g, i0, j0, acc);
+}
+
+// The b-th pair ti <= tj of a triangle, its rows one after another.
+__device__ __forceinline__ void triangle_tile(int b, int tiles, int& ti, int& tj) {
+  ti = 0;
+  for (int len = tiles; b >= len; --len) {
+    b -= len;
+    ++ti;
+  }
+  tj = ti + b;
+}
+
+// A = X X^T of few tiles and a long K: each tile's sum is cut along K into `parts`, whose
+// workgroups leave their accumulators in memory (a lane's next to its neighbours'), and
+// ns_gram_join adds them in order: else few CUs work through many slices, 60 ns each. All five
+// steps, whole sums and parts: 64 x 4099 150 and 108 us, two matrices of 256 x 4096 217 and 162,
+// three of 230 x 1878 155 and 139.
+template <class TILE>
+__global__ __launch_bounds__(TILE::THREADS) void ns_gram_part(ProductArgs p) {
+  extern __shared__ __align__(16) uint8_t s_lds[];
+  const int part = blockIdx.x % p.parts, tile = blockIdx.x / p.parts;
+  const int per_matrix = p.tiles_i * (p.tiles_i + 1) / 2;
+  int ti, tj;
+  triangle_tile(tile % per_matrix, p.tiles_i, ti, tj);
+  v16f acc[TILE::RI][TILE::RJ];
+  const int k0 = part * p.part_k;
+  tile_sum<kGram, TILE>(p, s_lds, tile / per_matrix, ti * TILE::T, tj * TILE::T, k0,
+                        min(p.part_k, p.K - k0), acc);
+  float* to = p.sums + (size_t)blockIdx.x * TILE::T * TILE::T + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < TILE::RI * TILE::RJ; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      to[(i * 16 + r) * TILE::THREADS] = acc[i / TILE::RJ][i % TILE::RJ][r];
+}
+
+template <class TILE>
+__global__ __launch_bounds__(TILE::THREADS) void ns_gram_join(ProductArgs p) {
+  constexpr int N = TILE::RI * TILE::RJ;
+  extern __shared__ __align__(16) uint8_t s_lds[];
+  const int tile = blockIdx.x, per_matrix = p.tiles_i * (p.tiles_i + 1) / 2;
+  int ti, tj;
+  triangle_tile(tile % per_matrix, p.tiles_i, ti, tj);
+  v16f acc[TILE::RI][TILE::RJ];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i / TILE::RJ][i % TILE::RJ][r] = 0.f;
+#pragma unroll 4  // four parts' loads under way at once
+  for (int part = 0; part < p.parts; ++part) {
+    const float* from =
+        p.sums + ((size_t)tile * p.parts + part) * TILE::T * TILE::T + threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        acc[i / TILE::RJ][i % TILE::RJ][r] += from[(i * 16 + r) * TILE::THREADS];
+  }
+  tile_write<kGram, TILE>(p, s_lds, tile / per_matrix, ti * TILE::T, tj * TILE::T, acc);
+}
+
 // All tiles of a product: `whole` of them in the tile's own size, the rest, which would be left
 // over for a round of their own on a few CUs, in quarters. The quarter below the diagonal of a
 // symmetric result's diagonal tile is its mirror's.
@@ -482,13 +564,8 @@ __global__ __launch_bounds__(TILE::THREADS) void ns_product(ProductArgs p) {
   const size_t g = b / per_matrix;
   b %= per_matrix;
   int ti, tj;
-  if constexpr (SYM) {  // the b-th pair i <= j, rows of the triangle one after another
-    ti = 0;
-    for (int len = p.tiles_i; b >= len; --len) {
-      b -= len;
-      ++ti;
-    }
-    tj = ti + b;
+  if constexpr (SYM) {
+    triangle_tile(b, p.tiles_i, ti, tj);
   } else {
     ti = b / p.tiles_j;
     tj = b % p.tiles_j;
@@ -547,7 +624,8 @@ Deal best_deal(int G, int rows, int cols, bool symmetric) {
 struct Workspace {
   int m, n, mp, np;
   Deal symmetric, apply;
-  size_t x, xt[2], a, p, norms, bytes;
+  int parts, part_k;  // of the sums of A = X X^T
+  size_t x, xt[2], a, p, norms, sums, bytes;
   Workspace(int G, int M, int N) {
     m = std::min(M, N);
     n = std::max(M, N);
@@ -569,7 +647,21 @@ struct Workspace {
     a = xt[1] + big;
     p = a + small;
     norms = p + small;
-    bytes = round_up(norms + (size_t)G * kNormBlocks * sizeof(double), 256);
+    sums = round_up(norms + (size_t)G * kNormBlocks * sizeof(double), 256);
+    // X X^T in parts of at least eight slices, no more workgroups than CUs, where that saves more
+    // than the parts' way through memory takes: a sum shorter by 56 or 64 slices is no
+    // faster (128 x 1024 95 us both, seven of 200 x 1500 164 and 168), by 88 it is (200 x 1500
+    // 132 and 125)
+    part_k = np;
+    const int slices = np / kSlice, tiles = symmetric.blocks;
+    if (symmetric.tile == Tile64::T && tiles <= 128) {
+      const int most = std::min(256 / tiles, slices / 8);
+      const int len = most > 1 ? cdiv(cdiv(slices, most), 4) * 4 : slices;
+      if (slices - len >= 72) part_k = len * kSlice;
+    }
+    parts = cdiv(np, part_k);
+    bytes = sums;
+    if (parts > 1) bytes += (size_t)tiles * parts * Tile64::T * Tile64::T * sizeof(float);
   }
   Split at(void* base, size_t off, int G, int rows, int k) const {
     _Float16* hi = reinterpret_cast<_Float16*>((char*)base + off);
@@ -666,16 +758,26 @@ mgg_status grouped_newton_schulz(mgg_act dt, mgg_act out_dt, int G, int M, int N
            : d.tile == 128 ? run_tile(Tile128{}, Quarter128{}, what, d, args)
                            : run_tile(Tile256{}, Quarter256{}, what, d, args);
   };
+  float* sums = reinterpret_cast<float*>((char*)workspace + ws.sums);
+  auto run_gram = [&](ProductArgs args) {
+    if (args.parts == 1) return run(std::integral_constant<Product, kGram>{}, args);
+    args.tiles_i = mp / Tile64::T;
+    const int tiles = ws.symmetric.blocks;
+    ns_gram_part<Tile64><<<tiles * args.parts, Tile64::THREADS, Tile64::LDS, stream>>>(args);
+    ns_gram_join<Tile64><<<tiles, Tile64::THREADS, Tile64::LDS, stream>>>(args);
+    return true;
+  };
   bool ok = true;
   for (int s = 0; s < steps && ok; ++s) {
-    const ProductArgs gram{x, x, np, 0, 0, 0, 1.f / (kScaleX * kScaleX), a, a, a,
-                           0.f, 0.f, 0.f, ns};
-    const ProductArgs poly{a, a, mp, 0, 0, 0, 1.f / (kScaleA * kScaleA), p, p, a,
+    const ProductArgs gram{x, x, np, 0, 0, 0, ws.part_k, ws.parts, sums,
+                           1.f / (kScaleX * kScaleX), a, a, a, 0.f, 0.f, 0.f, ns};
+    const ProductArgs poly{a, a, mp, 0, 0, 0, mp, 1, nullptr,
+                           1.f / (kScaleA * kScaleA), p, p, a,
                            coeffs[3 * s], coeffs[3 * s + 1], coeffs[3 * s + 2], ns};
-    const ProductArgs apply{p, xt, mp, 0, 0, 0, 1.f / (kScaleP * kScaleX), x, xt_next, a,
-                            0.f, 0.f, 0.f, ns};
+    const ProductArgs apply{p, xt, mp, 0, 0, 0, mp, 1, nullptr,
+                            1.f / (kScaleP * kScaleX), x, xt_next, a, 0.f, 0.f, 0.f, ns};
     using std::integral_constant;
-    ok = run(integral_constant<Product, kGram>{}, gram) &&
+    ok = run_gram(gram) &&
          run(integral_constant<Product, kPoly>{}, poly) &&
          (s + 1 < steps ? run(integral_constant<Product, kApply>{}, apply)
                         : run(integral_constant<Product, kLast>{}, apply));

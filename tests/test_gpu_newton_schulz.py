@@ -65,6 +65,17 @@ def test_sizes(G, M, N, dtype):
     check(momenta(G, M, N, dtype, rank=2))
 
 
+# Few tiles and a long K: the sums of X X^T are cut into parts, the last of them shorter or not.
+@pytest.mark.parametrize("G,M,N", [(1, 64, 4099), (1, 5000, 60), (3, 230, 1878), (7, 200, 1500),
+                                   (1, 449, 3000), (2, 2300, 380)])
+def test_long_sums(G, M, N):
+    say(f"ns long sums {G} {M} {N}")
+    X = momenta(G, M, N, torch.float32)
+    out = check(X)
+    assert torch.equal(out, mgg.grouped_newton_schulz(X.to(DEV)))
+    check(momenta(G, M, N, torch.bfloat16, rank=3))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 7])
 def test_steps_and_coefficients(steps):
     say(f"ns steps {steps}")
