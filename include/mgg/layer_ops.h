@@ -81,8 +81,8 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
 /*
  * Gradient of the logits, from the gradients of the weights and of the balance losses; counts
  * and ids carry none. Padding rows get 0. A NULL d_weights or d_balance counts as 0 (not
- * both). ids, counts and tokens are route_topk's (ids outside [0, G) are skipped); counts and
- * tokens may be NULL when d_balance is.
+ * both, unless T = 0). ids, counts and tokens are route_topk's (ids outside [0, G) are
+ * skipped); counts and tokens may be NULL when d_balance is.
  *   d_weights   float32 [T][k]; d_balance float32 [S].
  *   d_logits    [T][G] in the logits' type.
  */

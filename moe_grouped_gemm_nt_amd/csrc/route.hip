@@ -777,7 +777,8 @@ mgg_status route_topk_backward(mgg_act dt, int T, int G, int k, const void* logi
   mgg_set_last_error("");
   if (const char* err = check_route(dt, T, G, k, logits, ld, score, scale, S, seq_ends))
     return fail(MGG_EINVAL, err);
-  if (!d_weights && !d_balance)
+  // without rows d_weights has no elements, and its address may be 0
+  if (T > 0 && !d_weights && !d_balance)
     return fail(MGG_EINVAL, "one of d_weights and d_balance must be given");
   if (T > 0 && (!d_logits || (d_weights && !ids))) return fail(MGG_EINVAL, "null pointer");
   if (d_balance && (!counts || !tokens))
