@@ -328,13 +328,12 @@ def block_residual_norm(x, y, w_after=None, gate=None, scale=None, w_before=None
     import torch
     block = _block(x, y, w_after, gate, scale, w_before, alpha, beta, eps)
     T, H = x.shape
+    _mgg._require(u is None or w_before is not None, "u and w_before go together")
     lib = _mgg.load_library()
     _same_device(x, y, w_after, gate, scale, w_before, x_out, u)
     x_out = _given(x_out, (T, H), x.dtype, "x_out", x)
     if w_before is not None:
         u = _given(u, (T, H), x.dtype, "u", x)
-    else:
-        _mgg._require(u is None, "u and w_before go together")
     _run(lib.block_residual_norm, x.device, ctypes.byref(block), _ptr(x_out), _ptr(u))
     return x_out, u
 
