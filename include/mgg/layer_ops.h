@@ -164,9 +164,10 @@ mgg_status block_norm_backward(mgg_act dt, mgg_act param, int T, int H, const vo
  *   X = X / (|X|_F + eps);   for each step s:  A = X X^T,
  *   X = a_s X + (b_s A + c_s A A) X        (for M > N the same on the transposed matrix)
  *   out = scale * X.
- * Products are of float32 grade: each operand is held as the sum of two fp16 numbers and
- * multiplied as three fp16 matrix products with float32 accumulation. A matrix of zeros gives
- * zeros; a matrix with a NaN or infinity gives NaN and leaves the others alone.
+ * Products are of float32 grade, also where |X|_F is far below eps: each operand is held as the
+ * sum of two fp16 numbers, times a power of two of its matrix's and step's own, and multiplied as
+ * three fp16 matrix products with float32 accumulation. A matrix of zeros gives zeros; a matrix
+ * with a NaN or infinity gives NaN and leaves the others alone.
  *
  *   G, M, N     1 <= G <= 4096; 1 <= M, N <= 32768.
  *   X           [G][M][N] of `dt`; out [G][M][N] of `out_dt`. Either may be bf16 or float32.

@@ -13,8 +13,12 @@
 // directions, with them. Matrix instructions take 16-bit operands, so a value v is held as
 // two fp16 numbers, hi = fp16(v * 2^s) and lo = fp16(v * 2^s - hi), together 22 bits, and a
 // product is hi hi + hi lo + lo hi in one float32 accumulator (lo lo is below 2^-22 of it).
-// The power of two keeps hi and lo out of fp16's subnormal range: |X| <= 4 and |A| <= 16 take
-// 2^12, |P| <= 64 takes 2^10.
+// The power of two keeps them below fp16's largest and a matrix as a whole, relative to its
+// norm, clear of the 2^-24 at which fp16 ends below: |X| <= 4 and |A| <= 16 take 2^12, |P| <= 64
+// takes 2^10. Where a matrix is small (its norm next to eps, or coefficients that shrink it) X is
+// held 2^x times larger, A = X X^T by itself 2^2x times, and P 2^p times: x and p of each matrix
+// and step come from bounds that hold before the steps run (Growth), and are 0 where the bounds
+// are 1/2 or more.
 
 #include "layer_common.h"
 
@@ -77,7 +81,25 @@ struct NsArgs {
   float eps, scale;
   double* norms;   // [G][kNormBlocks], the first norm_blocks of each
   int norm_blocks;
+  int2* bits;      // [G][kMaxSteps + 1]: x and p of each step's X and P (above)
 };
+
+// What the steps do to singular values: `a`, `b`, `c` the sizes of the coefficients, `most` the
+// largest |P| and `top` the largest singular value that a step makes of those in its range.
+struct Growth {
+  int steps;
+  float a[kMaxSteps], b[kMaxSteps], c[kMaxSteps], most[kMaxSteps], top[kMaxSteps];
+};
+
+// The powers of two that a matrix of this norm at most is held larger by (NaN: none). Below
+// 2^-kMostBits nothing is left of a float32 result; P's factor stays a float.
+constexpr int kMostBits = 300, kMostBitsP = 110;
+__device__ __forceinline__ int spare_bits(double bound, int most) {
+  if (!(bound > 0.0)) return 0;
+  int exponent;
+  (void)frexp(bound, &exponent);
+  return min(max(-exponent, 0), most);
+}
 
 // Eight elements of the caller's matrix from `p`, which is aligned to an element only; `n` of them
 // exist.
@@ -151,8 +173,9 @@ __device__ __forceinline__ void store_eight(const Split& to, size_t at, const fl
 }
 
 // Scales a matrix to norm 1 and writes X and X^T in halves, padded with zeros: 64 x 64 values a
-// workgroup, eight of a row (then of a column, by way of LDS) a thread.
-__global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt) {
+// workgroup, eight of a row (then of a column, by way of LDS) a thread. One more row of workgroups
+// (blockIdx.y) writes `bits`.
+__global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Growth growth, Split x, Split xt) {
   // rows 65 words apart: the columns' readers meet different banks
   __shared__ float s_tile[kSplitTile][kSplitTile + 1];
   // every wave adds the partial sums in the same order
@@ -160,7 +183,23 @@ __global__ __launch_bounds__(kThreads) void ns_split(NsArgs a, Split x, Split xt
   for (int i = threadIdx.x & 63; i < a.norm_blocks; i += 64)
     sum += a.norms[(size_t)blockIdx.z * kNormBlocks + i];
   sum = lanes_sum<64>(sum);
-  const double inv = (double)kScaleX / (sqrt(sum) + (double)a.eps);
+  const double norm = sqrt(sum), to_one = norm + (double)a.eps;
+  const double inv = ldexp((double)kScaleX, spare_bits(norm / to_one, kMostBits)) / to_one;
+  if (blockIdx.y == gridDim.y - 1) {
+    // a workgroup of its own: the steps' bounds depend on each other
+    if (blockIdx.x != 0 || threadIdx.x != 0) return;
+    double bound = norm / to_one;  // of X's singular values before step s
+    for (int s = 0; s < growth.steps; ++s) {
+      const double t = bound * bound;
+      const double p = fmin((double)growth.most[s],
+                            growth.a[s] + t * (growth.b[s] + t * growth.c[s]));
+      a.bits[(size_t)blockIdx.z * (kMaxSteps + 1) + s] =
+          make_int2(spare_bits(bound, kMostBits), spare_bits(p, kMostBitsP));
+      bound = fmin((double)growth.top[s], bound * p);
+    }
+    a.bits[(size_t)blockIdx.z * (kMaxSteps + 1) + growth.steps] = make_int2(0, 0);
+    return;
+  }
   // the caller's rows run along tile rows here; `direct` has them as rows
   const Split direct = a.tall ? xt : x, turned = a.tall ? x : xt;
   const int r0 = blockIdx.y * kSplitTile, c0 = blockIdx.x * kSplitTile;
@@ -206,7 +245,8 @@ struct ProductArgs {
   // kPoly: P = ca I + cb A + cc A A
   Split a;
   float ca, cb, cc;
-  NsArgs ns;          // kLast
+  int step;
+  NsArgs ns;
 };
 
 // A T x T output tile by WI x WJ waves of (32 RI) x (32 RJ), S slices in LDS.
@@ -408,6 +448,17 @@ __device__ __forceinline__ void tile_sum(const ProductArgs& p, uint8_t* s_lds, s
   }
 }
 
+// The powers of two that X and P are held larger by, and that of the next step's X.
+struct Bits {
+  int x, p, x_next;
+};
+template <Product WHAT>
+__device__ __forceinline__ Bits bits_of(const ProductArgs& p, size_t g) {
+  if constexpr (WHAT == kGram) return Bits{0, 0, 0};  // A's power follows from X's
+  const int2* at = p.ns.bits + g * (kMaxSteps + 1) + p.step;
+  return Bits{at[0].x, at[0].y, at[1].x};
+}
+
 // Writes a tile's sums, in the caller's or the next product's form.
 template <Product WHAT, class TILE>
 __device__ __forceinline__ void tile_write(const ProductArgs& p, uint8_t* s_lds, size_t g, int i0,
@@ -424,6 +475,13 @@ __device__ __forceinline__ void tile_write(const ProductArgs& p, uint8_t* s_lds,
   uint32_t* turn = reinterpret_cast<uint32_t*>(s_lds + wave * TILE::TURN);
   constexpr int LD = TILE::TURN_LD;
   const bool mirror = !SYM || i0 != j0;
+  const Bits bits = bits_of<WHAT>(p, g);
+  const float a_true = ldexpf(1.f, -2 * bits.x);  // 0 where A is too small to show
+  const float cb = p.cb * a_true, cc = p.cc * a_true * a_true;
+  const float held = WHAT == kGram    ? kScaleA
+                     : WHAT == kPoly  ? ldexpf(kScaleP, bits.p)
+                     : WHAT == kApply ? ldexpf(kScaleX, bits.x_next - bits.x - bits.p)
+                                      : 0.f;
 #pragma unroll
   for (int i = 0; i < RI; ++i)
 #pragma unroll
@@ -443,14 +501,19 @@ __device__ __forceinline__ void tile_write(const ProductArgs& p, uint8_t* s_lds,
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float av = ((float)hi[e] + (float)lo[e]) * (1.f / kScaleA);
-            v[e] = fmaf(p.cc, v[e], p.cb * av) + (row == col + e ? p.ca : 0.f);
+            v[e] = fmaf(cc, v[e], cb * av) + (row == col + e ? p.ca : 0.f);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[4 * q + e] = WHAT == kLast ? __float_as_uint(v[e] * p.ns.scale)
-                                       : pack_halves(v[e] * (WHAT == kGram ? kScaleA
-                                                             : WHAT == kPoly ? kScaleP : kScaleX));
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (WHAT == kLast)
+            w[4 * q + e] = __float_as_uint(
+                bits.x + bits.p == 0
+                    ? v[e] * p.ns.scale
+                    : (float)ldexp((double)v[e] * (double)p.ns.scale, -bits.x - bits.p));
+          else
+            w[4 * q + e] = pack_halves(v[e] * held);
+        }
       }
       // each lane group reads back what other lanes of its own wave wrote
       const bool direct = WHAT != kLast || !p.ns.tall;
@@ -625,7 +688,7 @@ struct Workspace {
   int m, n, mp, np;
   Deal symmetric, apply;
   int parts, part_k;  // of the sums of A = X X^T
-  size_t x, xt[2], a, p, norms, sums, bytes;
+  size_t x, xt[2], a, p, norms, bits, sums, bytes;
   Workspace(int G, int M, int N) {
     m = std::min(M, N);
     n = std::max(M, N);
@@ -647,7 +710,8 @@ struct Workspace {
     a = xt[1] + big;
     p = a + small;
     norms = p + small;
-    sums = round_up(norms + (size_t)G * kNormBlocks * sizeof(double), 256);
+    bits = norms + (size_t)G * kNormBlocks * sizeof(double);
+    sums = round_up(bits + (size_t)G * (kMaxSteps + 1) * sizeof(int2), 256);
     // X X^T in parts of at least eight slices, no more workgroups than CUs, where that saves more
     // than the parts' way through memory takes: a sum shorter by 56 or 64 slices is no
     // faster (128 x 1024 95 us both, seven of 200 x 1500 164 and 168), by 88 it is (200 x 1500
@@ -670,9 +734,11 @@ struct Workspace {
 };
 
 // The largest |x p(x^2)| that the steps reach from singular values in [0, 1], and of the
-// polynomial P that multiplies X: a bound from the ends and the stationary points.
-bool stays_in_range(int steps, const float* coeffs) {
+// polynomial P that multiplies X: a bound from the ends and the stationary points. False where
+// they leave the range of the halves.
+bool stays_in_range(int steps, const float* coeffs, Growth& growth) {
   double top = 1.0;
+  growth.steps = steps;
   for (int s = 0; s < steps; ++s) {
     const double a = coeffs[3 * s], b = coeffs[3 * s + 1], c = coeffs[3 * s + 2];
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
@@ -693,6 +759,11 @@ bool stays_in_range(int steps, const float* coeffs) {
       if (t > 0.0 && t < top * top) p_top = std::max(p_top, std::fabs(poly(t)));
     }
     if (!(next <= 3.9) || !(p_top <= 60.0)) return false;
+    growth.a[s] = std::fabs(coeffs[3 * s]);
+    growth.b[s] = std::fabs(coeffs[3 * s + 1]);
+    growth.c[s] = std::fabs(coeffs[3 * s + 2]);
+    growth.most[s] = (float)p_top;
+    growth.top[s] = (float)next;
     top = std::max(next, 1e-3);
   }
   return true;
@@ -722,7 +793,8 @@ mgg_status grouped_newton_schulz(mgg_act dt, mgg_act out_dt, int G, int M, int N
     return fail(MGG_EINVAL, "X and out must be aligned to their element");
   if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(scale))
     return fail(MGG_EINVAL, "eps must be positive, eps and scale finite");
-  if (!stays_in_range(steps, coeffs))
+  Growth growth{};
+  if (!stays_in_range(steps, coeffs, growth))
     return fail(MGG_EUNSUPPORTED, "the coefficients send singular values out of range");
   const Workspace ws(G, M, N);
   if (!workspace || workspace_bytes < ws.bytes)
@@ -735,10 +807,12 @@ mgg_status grouped_newton_schulz(mgg_act dt, mgg_act out_dt, int G, int M, int N
   const Split a = ws.at(workspace, ws.a, G, mp, mp), p = ws.at(workspace, ws.p, G, mp, mp);
   const NsArgs ns{X, out, dt == MGG_ACT_BF16, out_dt == MGG_ACT_BF16, M, N, M > N, eps, scale,
                   reinterpret_cast<double*>((char*)workspace + ws.norms),
-                  (int)std::min<long>(kNormBlocks, ((long)M * N + 4095) / 4096)};
+                  (int)std::min<long>(kNormBlocks, ((long)M * N + 4095) / 4096),
+                  reinterpret_cast<int2*>((char*)workspace + ws.bits)};
   ns_norm<<<dim3(ns.norm_blocks, G), kThreads, 0, stream>>>(ns);
   const int rows = M > N ? np : mp, cols = M > N ? mp : np;
-  ns_split<<<dim3(cols / kSplitTile, rows / kSplitTile, G), kThreads, 0, stream>>>(ns, x, xt);
+  ns_split<<<dim3(cols / kSplitTile, rows / kSplitTile + 1, G), kThreads, 0, stream>>>(
+      ns, growth, x, xt);
   auto run_tile = [&](auto tile, auto quarter, auto what, const Deal& deal, ProductArgs args) {
     using TILE = decltype(tile);
     args.tiles_i = mp / TILE::T;
@@ -770,12 +844,12 @@ mgg_status grouped_newton_schulz(mgg_act dt, mgg_act out_dt, int G, int M, int N
   bool ok = true;
   for (int s = 0; s < steps && ok; ++s) {
     const ProductArgs gram{x, x, np, 0, 0, 0, ws.part_k, ws.parts, sums,
-                           1.f / (kScaleX * kScaleX), a, a, a, 0.f, 0.f, 0.f, ns};
+                           1.f / (kScaleX * kScaleX), a, a, a, 0.f, 0.f, 0.f, s, ns};
     const ProductArgs poly{a, a, mp, 0, 0, 0, mp, 1, nullptr,
                            1.f / (kScaleA * kScaleA), p, p, a,
-                           coeffs[3 * s], coeffs[3 * s + 1], coeffs[3 * s + 2], ns};
+                           coeffs[3 * s], coeffs[3 * s + 1], coeffs[3 * s + 2], s, ns};
     const ProductArgs apply{p, xt, mp, 0, 0, 0, mp, 1, nullptr,
-                            1.f / (kScaleP * kScaleX), x, xt_next, a, 0.f, 0.f, 0.f, ns};
+                            1.f / (kScaleP * kScaleX), x, xt_next, a, 0.f, 0.f, 0.f, s, ns};
     using std::integral_constant;
     ok = run_gram(gram) &&
          run(integral_constant<Product, kPoly>{}, poly) &&
