@@ -586,6 +586,10 @@ int threads_backward(int H, int vec) {
 // kernels' registers allow, and what the forward kernels' LDS leaves room for on wide rows.
 int resident_groups(int tpr) { return 256 * 1024 / tpr; }
 
+// Most workgroups of the forward kernels that do not keep the parameters: a launch holds fewer than
+// 2^32 threads. Further rows are walked.
+constexpr int kMostBlocks = 1 << 20;
+
 // Workgroups of the backward kernel, each with its own column sums: one round of resident ones,
 // with at least two rows for each of a workgroup's groups where there are as many, so that the
 // sums' traffic stays small next to the rows'.
@@ -699,8 +703,8 @@ mgg_status run_forward(mgg_act dt, const NormArgs& a, hipStream_t stream) {
         ok = launch(norm_forward<T, tpr(), nv(), BLOCK, true, whole()>, groups / per, threads,
                     staged_bytes(a.H, kVec<T>), a, stream);
       else
-        ok = launch(norm_forward<T, tpr(), nv(), BLOCK, false, whole()>, cdiv(a.T, per), threads,
-                    0, a, stream);
+        ok = launch(norm_forward<T, tpr(), nv(), BLOCK, false, whole()>,
+                    std::min(cdiv(a.T, per), kMostBlocks), threads, 0, a, stream);
     });
   };
   if (dt == MGG_ACT_BF16) go(bf16_t{});

@@ -32,3 +32,46 @@ def test_a_batch_without_rows(dtype):
         got = mgg.block_residual_norm_backward(x, x, d_u=x, gate=gate, scale=p, w_after=p,
                                                w_before=p)
         assert not any(g.any() for g in got[3:])
+
+
+def test_more_wide_rows_than_a_grid_has_threads_for():
+    """2^22 rows of more than 8192 columns: a workgroup of 1024 threads for each row would be
+    2^32 threads, which a launch does not hold (it took what was left past them, and seventy times
+    as long). Right, and in no more than four times the time of a fourth of the rows, twice over
+    for what else uses the memory meanwhile."""
+    H, most = 8200, (1 << 22) + 3
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB")
+    x = torch.zeros((most, H), dtype=torch.bfloat16, device=DEV)
+    u = torch.empty((most, H), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(0)
+    some = torch.tensor([0, 1, 5000, (1 << 20) - 1, 1 << 20, (1 << 22) - 1, 1 << 22, most - 1])
+    rows = torch.randn((len(some), H), generator=g).to(torch.bfloat16).to(DEV)
+    x[some.to(DEV)] = rows
+    w = (1 + 0.1 * torch.randn(H, generator=g)).to(DEV)
+
+    def timed(T):
+        mgg.block_norm(x[:T], w, u=u[:T])
+        start, stop = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        mgg.block_norm(x[:T], w, u=u[:T])
+        stop.record()
+        torch.cuda.synchronize()
+        return start.elapsed_time(stop)
+
+    say(f"block norm {1 << 20} rows of {H}")
+    fourth = timed(1 << 20)
+    for T in (most, 1 << 22):
+        say(f"block norm {T} rows of {H}")
+        u.fill_(7.0)
+        assert timed(T) <= 2 * 4 * fourth
+        at = some[some < T].to(DEV)
+        assert torch.equal(u[at], mgg.block_norm(rows[:len(at)], w))
+        # all others are rows of zeros
+        u[at] = 0
+        for part in u[:T].split(1 << 19):
+            assert not part.any()
+        assert (u[T:] == 7).all()
+    del x, u, part
+    torch.cuda.empty_cache()
