@@ -101,7 +101,8 @@ mgg_status route_topk_backward(mgg_act dt, int T, int G, int k, const void* logi
  *   x_out = alpha * x + beta * scale[c] * g * z               (scale NULL: 1)
  *   u     = rms(x_out; w_before)                              (x_out before its rounding)
  *
- *   0 <= T <= 2^30; 1 <= H <= 32768; eps > 0; alpha, beta finite.
+ *   0 <= T <= 2^30; 1 <= H <= 32768; eps > 0, not subnormal; alpha, beta finite.
+ *   The squares of a row sum to less than float32's largest, 3.4e38.
  *   x, y        [T] rows of H; gate: [T] values (MGG_GATE_TOKEN, ld_gate the step from one to
  *               the next, >= 1) or [T] rows of H (MGG_GATE_ELEMENT), in the activations' type.
  *   scale, w_after, w_before   [H] of `param`, or NULL.

@@ -649,7 +649,9 @@ const char* check_block(const NormArgs& a, mgg_act dt, mgg_act param, bool block
   if (!known(dt) || !known(param)) return "unknown element type";
   if (a.T < 0 || a.T > kMaxRows) return "T must be in [0, 2^30]";
   if (a.H < 1 || a.H > kMaxH) return "H must be in [1, 32768]";
-  if (!(a.eps > 0.f) || !std::isfinite(a.eps)) return "eps must be positive and finite";
+  // from a subnormal eps on the square of 1 / sqrt(eps) is infinite
+  if (!(a.eps >= 1.17549435e-38f) || !std::isfinite(a.eps))
+    return "eps must be positive, normal and finite";
   if (!std::isfinite(a.alpha) || !std::isfinite(a.beta)) return "alpha and beta must be finite";
   const size_t e = elem_bytes(dt), p = elem_bytes(param);
   if (a.T > 0 && !a.x) return "null pointer";
