@@ -136,7 +136,8 @@ __device__ __forceinline__ float row_max(const float (&l)[V]) {
 template <int L>
 constexpr int kCandidates = 2 * L;
 
-// The chosen of a row as a lane holds them: `id` at place `rank` (>= k: none), with its hat.
+// The chosen of a row as a lane holds them: `id` at place `rank` (>= k: none), with its hat, or with
+// its logit where a bias chose it.
 template <int L>
 struct Chosen {
   static constexpr int N = 2;  // places lane and lane + L; kMaxTopk <= 2 L
@@ -315,18 +316,31 @@ __device__ __forceinline__ void route_row(const RouteArgs& a, const T* row, int 
       for (int v = 0; v < V; ++v) acc[v] = fmaf(hat[v], inv_sum, acc[v]);
     }
   }
-  auto hat_of = [&](float logit) { return sc.hat(logit); };
+  auto hat_of = [&](float logit) { return BIAS ? logit : sc.hat(logit); };
   Chosen<L> c;
   if (!choose_by_candidates<T, L, V, SIGMOID, BIAS>(a, row, lane, l, hat, bias, sc.to_q, hat_of,
                                                     s_id, s_order, c))
     c = choose_by_rounds<T, L, V, BIAS>(a, row, lane, l, hat_of);
+  float to_q = sc.to_q;
+  if constexpr (BIAS) {
+    // a bias may choose experts so far below the row's best that nothing is left of their hats:
+    // their shares come from their own best
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < c.N; ++i)
+      if (c.rank[i] < a.k && c.id[i] >= 0) top = fmaxf(top, c.hat[i]);
+    const Scores<SIGMOID> own(lanes_reduce<L>(top, [](float x, float y) { return fmaxf(x, y); }));
+#pragma unroll
+    for (int i = 0; i < c.N; ++i) c.hat[i] = c.id[i] < 0 ? 0.f : own.hat(c.hat[i]);
+    to_q = own.to_q;
+  }
   float chosen = 0.f;
 #pragma unroll
   for (int i = 0; i < c.N; ++i) chosen += c.rank[i] < a.k ? c.hat[i] : 0.f;
   chosen = lanes_sum<L>(chosen);
   const float to_w =
       a.scale * (a.renormalize ? (chosen == 0.f ? 0.f : 1.f / chosen)
-                               : (SIGMOID ? sc.to_q : inv_sum));
+                               : (SIGMOID ? to_q : inv_sum));
 #pragma unroll
   for (int i = 0; i < c.N; ++i)
     if (active && c.rank[i] < a.k) {
@@ -507,16 +521,25 @@ struct RouteGradArgs {
   int rows_per_block;
 };
 
+constexpr uint32_t kNone = 0xffffffffu;  // a NaN that no gradient is stored as
+
+__device__ __forceinline__ uint32_t gradient_bits(float d) {
+  return d != d ? 0x7fc00000u : __float_as_uint(d);
+}
+
 // d_l = p (b - sum p b) [(1 - q) for sigmoid], b_e = d_balance G c_e / (k n^2), plus on the
 // chosen experts the gradient that reaches them through the weights: with pi = hat / Q the
 // shares of the chosen (Q the sum of their hats),
 //   renormalised: scale * pi * (dw - sum pi dw)    [(1 - q) for sigmoid]
 //   otherwise:    scale * dw enters b (softmax), or scale * dw q (1 - q) (sigmoid).
+// Waves for each SIMD that the compiler is held to: with sigmoid scores and 16 slots it would take 136
+// registers and lose one of four.
+constexpr int grad_waves(int V) { return V <= 8 ? 5 : V <= 16 ? 4 : V <= 20 ? 3 : 1; }
+
 template <class T, class SHAPE, bool SIGMOID>
-__global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
+__global__ __launch_bounds__(kThreads, grad_waves(SHAPE::V)) void route_grad(RouteGradArgs a) {
   __shared__ int s_found[kThreads / 64];
   constexpr int L = SHAPE::L, V = SHAPE::V, RP = kThreads / L;
-  constexpr uint32_t kNone = 0xffffffffu;  // a NaN that no gradient is stored as
   // rows 16 words apart modulo the 64 banks
   __shared__ uint32_t s_dw[RP][L * V + (L < 64 ? 16 : 0)];
   const int lane = threadIdx.x & (L - 1), grp = threadIdx.x / L;
@@ -584,7 +607,7 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           if ((unsigned)in.id[i] < (unsigned)a.G)
-            s_dw[grp][in.id[i]] = in.dw[i] != in.dw[i] ? 0x7fc00000u : __float_as_uint(in.dw[i]);
+            s_dw[grp][in.id[i]] = gradient_bits(in.dw[i]);
         wave_order();
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -633,6 +656,41 @@ __global__ __launch_bounds__(kThreads) void route_grad(RouteGradArgs a) {
         float d = h[v] * ((b0[v] - mean_b) * inv_sum + g[v]);
         if constexpr (SIGMOID) d *= Scores<SIGMOID>::one_minus_q(l[v]);
         if (active && (v < SHAPE::FULL || e < a.G)) out[tr * a.G + e] = from_f32<T>(d);
+      }
+      // Chosen by a bias, far below the row's best: little or nothing may be left of their hats, and
+      // their shares come from their own best. The same for all lanes of a row. The choices' lanes
+      // write their experts' gradients again, after the slots' lanes of the same wave.
+      if (SIGMOID && a.renormalize && a.d_weights != nullptr && q_sum < 0.0625f) {
+        float own_l[2], own_h[2], top = -INFINITY, own_sum = 0.f, own_dw = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          own_l[i] = (unsigned)in.id[i] < (unsigned)a.G
+                         ? to_f32(reinterpret_cast<const T*>(a.logits)[tr * a.ld + in.id[i]])
+                         : -INFINITY;
+          top = fmaxf(top, own_l[i]);
+        }
+        const Scores<SIGMOID> own(
+            lanes_reduce<L>(top, [](float x, float y) { return fmaxf(x, y); }));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          own_h[i] = own.hat(own_l[i]);  // 0 where there is no choice
+          own_sum += own_h[i];
+          own_dw += own_h[i] * in.dw[i];
+        }
+        own_sum = lanes_sum<L>(own_sum);
+        const float inv = own_sum == 0.f ? 0.f : 1.f / own_sum;
+        own_dw = lanes_sum<L>(own_dw) * inv;
+        wave_order();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!active || (unsigned)in.id[i] >= (unsigned)a.G) continue;
+          const float b = a.d_balance != nullptr
+                              ? per_count * (float)a.counts[(size_t)s * a.G + in.id[i]] : 0.f;
+          const float d = sc.hat(own_l[i]) * ((b - mean_b) * inv_sum) +
+                          a.scale * inv * own_h[i] * (in.dw[i] - own_dw);
+          out[tr * a.G + in.id[i]] = from_f32<T>(d * Scores<SIGMOID>::one_minus_q(own_l[i]));
+        }
+        wave_order();
       }
     }
     row = end;
