@@ -709,14 +709,18 @@ int rows_per_block(int T, int G, int most) {
 int row_blocks(int T, int rows) { return T > 0 ? cdiv(T, rows) : 1; }
 
 // Calls f with the shape that holds G in the fewest slots. Up to 320 experts 16 lanes share a row
-// (four rows to a wave); beyond that a row takes more lanes, so that its logits still fit the
-// registers.
+// (four rows to a wave), with two slots more for every 32 experts; beyond that a row takes more
+// lanes, so that its logits still fit the registers, and the slots double.
 template <class F>
 void with_shape(int G, F f) {
-  if (G <= 64) return f(ShapeOf<16, 4, 0>{});
-  if (G <= 128) return f(ShapeOf<16, 8, 4>{});
-  if (G <= 192) return f(ShapeOf<16, 12, 8>{});
-  if (G <= 256) return f(ShapeOf<16, 16, 12>{});
+  if (G <= 32) return f(ShapeOf<16, 2, 0>{});
+  if (G <= 64) return f(ShapeOf<16, 4, 2>{});
+  if (G <= 96) return f(ShapeOf<16, 6, 4>{});
+  if (G <= 128) return f(ShapeOf<16, 8, 6>{});
+  if (G <= 160) return f(ShapeOf<16, 10, 8>{});
+  if (G <= 192) return f(ShapeOf<16, 12, 10>{});
+  if (G <= 224) return f(ShapeOf<16, 14, 12>{});
+  if (G <= 256) return f(ShapeOf<16, 16, 14>{});
   if (G <= 288) return f(ShapeOf<16, 18, 16>{});
   if (G <= 320) return f(ShapeOf<16, 20, 18>{});
   if (G <= 512) return f(ShapeOf<32, 16, 10>{});
