@@ -25,10 +25,13 @@ constexpr int kThreads = 256;
 constexpr int kMaxTopk = 32;
 constexpr int kMaxExperts = 4096;
 constexpr int kMaxSequences = 65535;  // grid.y of the summing kernel
-// Most workgroups that rows are dealt to, for each of the 256 CUs: four, or two where a workgroup
-// has a start and an end to pay for (counts and sums: below kLongChunk rows each) or the
-// registers allow no more (selection with a bias).
-constexpr int kRowBlocks = 1024, kRowBlocksFew = 512, kLongChunk = 64;
+// Most workgroups that rows are dealt to: four for each of the 256 CUs, or two in a forward kernel with
+// counts whose registers leave room for fewer than four waves a SIMD. 65536 rows with two and with four:
+// selection with counts of 128 by softmax 27 and 23 us, of 288 36 and 31; by sigmoid with bias of
+// 128 42 and 33, of 288 (three waves) 53 and 56, 16384 rows 25 and 31. In the gradient's kernels with
+// three waves neither is better throughout (288 by sigmoid: 16384 rows of float32 16 and 19 us,
+// 131072 of bf16 73 and 67).
+constexpr int kRowBlocks = 1024, kRowBlocksFew = 512;
 
 struct RouteArgs {
   const void* logits;
@@ -699,6 +702,10 @@ __global__ __launch_bounds__(kThreads, grad_waves(SHAPE::V)) void route_grad(Rou
     out[i] = from_f32<T>(0.f);
 }
 
+// Whether fewer than four waves a SIMD fit (128 registers each) a forward kernel: with counts it keeps
+// two arrays of a row's V slots, and with a bias two more.
+constexpr bool few_blocks(int V, bool biased, bool stats) { return stats && V > (biased ? 12 : 20); }
+
 // Rows a workgroup takes: whole passes of kThreads / L rows, and no more workgroups than
 // `most`, so that partials stay few next to the logits.
 int rows_per_block(int T, int G, int most) {
@@ -785,10 +792,8 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
     return fail(MGG_EINVAL, "counts, tokens and balance are given together");
   if (!aligned(counts, 4) || !aligned(tokens, 4) || !aligned(balance, 4))
     return fail(MGG_EINVAL, "counts, tokens and balance must be 4-byte aligned");
-  const bool few = bias || (stats && T < kRowBlocks * kLongChunk);
-  const int rows = rows_per_block(T, G, few ? kRowBlocksFew : kRowBlocks);
-  RouteArgs a{logits, ld,       bias, T,       G,    k,       S,       renormalize,
-              scale,  seq_ends, ids,  weights, rows, nullptr, nullptr, nullptr};
+  RouteArgs a{logits, ld,       bias, T,       G, k,       S,       renormalize,
+              scale,  seq_ends, ids,  weights, 0, nullptr, nullptr, nullptr};
   double* dots = nullptr;
   if (stats) {
     const Workspace ws(T, G, S);
@@ -803,12 +808,14 @@ mgg_status route_topk(mgg_act dt, int T, int G, int k, const void* logits, int64
   } else if (T == 0) {
     return MGG_OK;
   }
-  const dim3 grid((unsigned)row_blocks(T, rows));
   const size_t lds = stats ? (size_t)G * 8 : 0;
   const bool sigmoid = score == MGG_SCORE_SIGMOID;
   with_shape(G, [&](auto shape) {
     using SHAPE = decltype(shape);
     auto go = [&](auto elem, auto sig, auto biased, auto with_stats) {
+      constexpr bool few = few_blocks(SHAPE::V, biased(), with_stats());
+      a.rows_per_block = rows_per_block(T, G, few ? kRowBlocksFew : kRowBlocks);
+      const dim3 grid((unsigned)row_blocks(T, a.rows_per_block));
       route_rows<decltype(elem), SHAPE, sig(), biased(), with_stats()>
           <<<grid, kThreads, lds, stream>>>(a);
     };

@@ -1,5 +1,5 @@
-"""Routing of a training batch: row counts on both sides of the size from which rows are dealt to
-more workgroups, ragged sequences with padded ends, counts and losses and both gradients. Tolerances
+"""Routing of a training batch: more rows than one pass of all workgroups, ragged sequences with
+padded ends, counts and losses and both gradients. Tolerances
 are those of test_gpu_route.py (a lane adds at most cdiv(T, 512) / 4 rows of a workgroup, 36 at
 most here, of the 128 roundings that its sums over rows are given)."""
 
