@@ -601,16 +601,20 @@ int row_blocks(int T, int tpr) {
 
 // Whether workgroups keep the columns' parameters in LDS: when each takes several rows, and two
 // workgroups' vectors fit a CU.
-bool staged(int T, int H, int groups) { return H <= 8192 && T >= 4 * groups; }
+constexpr int kStagedH = 8192;
+bool staged(int T, int H, int groups) { return H <= kStagedH && T >= 4 * groups; }
+// Whether rows of a shape can be that short: those with more than one piece a thread hold more pieces
+// than the shape with half as many.
+constexpr bool may_stage(int tpr, int nv, int vec) { return nv == 1 || tpr * (nv / 2) * vec < kStagedH; }
 size_t staged_bytes(int H, int vec) { return (size_t)cdiv(H, vec) * vec * 2 * sizeof(float); }
 
 // Calls f(threads to a row, pieces a thread, whether H is whole pieces) as compile-time constants.
-template <bool BACKWARD, class F>
-void with_shape(int H, int vec, F f) {
+template <bool BACKWARD, int VEC, class F>
+void with_shape(int H, F f) {
   using std::integral_constant;
-  const int tpr = BACKWARD ? threads_backward(H, vec) : threads_forward(H, vec);
-  const int nv = cdiv(H, tpr * vec);
-  const bool whole = H % vec == 0;
+  const int tpr = BACKWARD ? threads_backward(H, VEC) : threads_forward(H, VEC);
+  const int nv = cdiv(H, tpr * VEC);
+  const bool whole = H % VEC == 0;
 #define MGG_SHAPE(TPR, NV)                                                                      \
   if (tpr == TPR && nv <= NV)                                                                   \
   return whole                                                                                  \
@@ -629,7 +633,9 @@ void with_shape(int H, int vec, F f) {
   }
   MGG_SHAPE(1024, 2);
   MGG_SHAPE(1024, 4);
-  MGG_SHAPE(1024, 8);
+  if constexpr (1024 * 4 * VEC < kMaxH) {
+    MGG_SHAPE(1024, 8);
+  }
 #undef MGG_SHAPE
 }
 
@@ -698,15 +704,18 @@ mgg_status run_forward(mgg_act dt, const NormArgs& a, hipStream_t stream) {
   bool ok = true;
   auto go = [&](auto elem) {
     using T = decltype(elem);
-    with_shape<false>(a.H, kVec<T>, [&](auto tpr, auto nv, auto whole) {
+    with_shape<false, kVec<T>>(a.H, [&](auto tpr, auto nv, auto whole) {
       constexpr int threads = block_threads(tpr()), per = threads / tpr();
       const int groups = resident_groups(tpr());
-      if (staged(a.T, a.H, groups))
-        ok = launch(norm_forward<T, tpr(), nv(), BLOCK, true, whole()>, groups / per, threads,
-                    staged_bytes(a.H, kVec<T>), a, stream);
-      else
-        ok = launch(norm_forward<T, tpr(), nv(), BLOCK, false, whole()>,
-                    std::min(cdiv(a.T, per), kMostBlocks), threads, 0, a, stream);
+      if constexpr (may_stage(tpr(), nv(), kVec<T>)) {
+        if (staged(a.T, a.H, groups)) {
+          ok = launch(norm_forward<T, tpr(), nv(), BLOCK, true, whole()>, groups / per, threads,
+                      staged_bytes(a.H, kVec<T>), a, stream);
+          return;
+        }
+      }
+      ok = launch(norm_forward<T, tpr(), nv(), BLOCK, false, whole()>,
+                  std::min(cdiv(a.T, per), kMostBlocks), threads, 0, a, stream);
     });
   };
   if (dt == MGG_ACT_BF16) go(bf16_t{});
@@ -734,15 +743,18 @@ mgg_status run_backward(mgg_act dt, NormArgs a, float* d_scale, float* d_w_after
     if (d_w_before) a.part_before = part;
     if (d_scale || d_w_after) a.part_block = part + round_up((size_t)blocks * a.H, 64);
     if (a.T == 0) return;
-    with_shape<true>(a.H, vec, [&](auto tpr, auto nv, auto whole) {
+    with_shape<true, vec>(a.H, [&](auto tpr, auto nv, auto whole) {
       constexpr int threads = block_threads(tpr());
       auto go = [&](auto what) {
-        if (staged(a.T, a.H, blocks * (threads / tpr())))
-          ok = launch(norm_backward<T, tpr(), nv(), what(), true, whole()>, blocks, threads,
-                      staged_bytes(a.H, vec), a, stream);
-        else
-          ok = launch(norm_backward<T, tpr(), nv(), what(), false, whole()>, blocks, threads, 0, a,
-                      stream);
+        if constexpr (may_stage(tpr(), nv(), vec)) {
+          if (staged(a.T, a.H, blocks * (threads / tpr()))) {
+            ok = launch(norm_backward<T, tpr(), nv(), what(), true, whole()>, blocks, threads,
+                        staged_bytes(a.H, vec), a, stream);
+            return;
+          }
+        }
+        ok = launch(norm_backward<T, tpr(), nv(), what(), false, whole()>, blocks, threads, 0, a,
+                    stream);
       };
       using std::integral_constant;
       if constexpr (!BLOCK) go(integral_constant<int, 0>{});
