@@ -63,7 +63,9 @@ typedef enum { MGG_GATE_NONE = 0, MGG_GATE_TOKEN = 1, MGG_GATE_ELEMENT = 2 } mgg
  *   balance[s] = sum_e (G c_s[e] / (k n_s)) * (sum_{t in s} p[t, e] / n_s),  0 if n_s = 0:
  * 1 when both are even over the experts.
  *
- *   T, G, k     0 <= T <= 2^30; 1 <= G <= 4096; 1 <= k <= min(G, 32).
+ *   T, G, k     0 <= T <= 2^30; 1 <= G <= 4096; 1 <= k <= min(G, 32). Up to 320 experts a choice
+ *               of more than about 10 takes several times as long as one of 8, with a bias
+ *               several tens of times from 16 on.
  *   logits      [T] rows of G (ld >= G).      bias  float32 [G] or NULL (sigmoid only).
  *   seq_ends    device int32 [S] or NULL, read by the kernels on every launch; S <= 65535.
  *   scale       finite.
@@ -102,7 +104,8 @@ mgg_status route_topk_backward(mgg_act dt, int T, int G, int k, const void* logi
  *   u     = rms(x_out; w_before)                              (x_out before its rounding)
  *
  *   0 <= T <= 2^30; 1 <= H <= 32768; eps > 0, not subnormal; alpha, beta finite.
- *   The squares of a row sum to less than float32's largest, 3.4e38.
+ *   The squares of a row sum to less than float32's largest, 3.4e38. Rows wider than 16384 in
+ *   bfloat16 or 8192 in float32 take up to four times as long for their bytes as others.
  *   x, y        [T] rows of H; gate: [T] values (MGG_GATE_TOKEN, ld_gate the step from one to
  *               the next, >= 1) or [T] rows of H (MGG_GATE_ELEMENT), in the activations' type.
  *   scale, w_after, w_before   [H] of `param`, or NULL.
