@@ -563,8 +563,7 @@ __device__ __forceinline__ void triangle_tile(int b, int tiles, int& ti, int& tj
 // workgroups leave their accumulators in memory (a lane's next to its neighbours'), and
 // ns_gram_join adds them in order: else few CUs work through many slices, 60 ns each. All five
 // steps, whole sums and parts: 64 x 4099 150 and 108 us, two matrices of 256 x 4096 217 and 162,
-// three of 230 x 1878 155 and 139 (2 us more
-// each since the powers of two).
+// three of 230 x 1878 155 and 139 (now 2 us more each, for the powers of two).
 template <class TILE>
 __global__ __launch_bounds__(TILE::THREADS) void ns_gram_part(ProductArgs p) {
   extern __shared__ __align__(16) uint8_t s_lds[];

@@ -90,3 +90,30 @@ def test_steps_without_a_linear_term(norm):
             least = 2.0 ** -126 * x.size ** 0.5  # of values below float32's range
             assert np.linalg.norm(got[g] - x) <= 4 * 6 * 3 ** (steps - 1) * 2.0 ** -22 \
                 * np.linalg.norm(x) + least
+
+
+def test_matrices_beyond_32_bits():
+    """More than 2^32 elements in one call: the last matrices, some of them far below eps, against
+    the same in a call of their own (other tiles, so other orders of the sums: each is within the
+    bound of float32 products in five steps, five times 2^-22 (|a| + |b| + |c|) twice over)."""
+    G, N, last = 1050, 2048, 3
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 150 << 30:
+        pytest.skip("needs 150 GB")
+    say(f"ns {G} {N} {N}")
+    X = torch.zeros((G, N, N), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    X[-last:] = (1e-3 * torch.randn((last, N, N), device=DEV, generator=g)).to(torch.bfloat16)
+    X[-2] *= 2.0 ** -40
+    X[0] = X[-1]
+    out = mgg.grouped_newton_schulz(X)
+    torch.cuda.synchronize()
+    assert torch.equal(out[0], out[-1])
+    for part in out[1:-last].split(64):
+        assert not part.any()
+    got, own = out[-last:].double(), mgg.grouped_newton_schulz(X[-last:].contiguous()).double()
+    for i in range(last):
+        allowed = 2 * 5 * 2.0 ** -22 * 10.251 + 2.0 ** -8  # and half a bf16 step of each
+        assert (got[i] - own[i]).norm() <= allowed * own[i].norm() and own[i].norm() > 0
+    del X, out, part
+    torch.cuda.empty_cache()
