@@ -26,6 +26,10 @@ block, orthogonalised expert updates; include/mgg/layer_ops.h) are bound in laye
 exported here too:
     route_topk, route_topk_backward, block_norm, block_norm_backward, block_residual_norm,
     block_residual_norm_backward, grouped_newton_schulz
+So are a whole MoE layer for the few tokens of a decoding step (few_tokens.py,
+include/mgg/few_tokens.h) and the dense products with bias, activation and residual in their
+epilogue (linear.py, include/mgg/linear.h):
+    moe_few_tokens, linear_act, linear_act_backward
 
 Element types: bfloat16 tensors select BF16; uint8 (or float8_e4m3fn) tensors select
 FP8 E4M3; FP8 activations with weights of K/2 bytes per row (uint8 or float4_e2m1fn_x2)
@@ -54,6 +58,9 @@ __all__ = [
     "block_residual_norm",
     "block_residual_norm_backward",
     "grouped_newton_schulz",
+    "moe_few_tokens",
+    "linear_act",
+    "linear_act_backward",
     "library_path",
     "load_library",
     "MggError",
@@ -109,6 +116,8 @@ def load_library() -> ctypes.CDLL:
               lib.swiglu_quant_fp8_1x128, lib.grouped_gemm_contiguous_swiglu_quant):
         f.restype = ctypes.c_int
     layer_ops.declare(lib)
+    few_tokens.declare(lib)
+    linear.declare(lib)
     lib.mgg_status_string.argtypes = [ctypes.c_int]
     lib.mgg_status_string.restype = ctypes.c_char_p
     lib.mgg_last_error.argtypes = []
@@ -392,7 +401,8 @@ def _quant(swiglu, X, Q, SF, sf_fmt, sf_zero):
     return Q, SF
 
 
-from . import layer_ops  # noqa: E402  (it uses the helpers above)
+from . import few_tokens, layer_ops, linear  # noqa: E402  (they use the helpers above)
+from .few_tokens import moe_few_tokens  # noqa: E402
 from .layer_ops import (  # noqa: E402
     block_norm,
     block_norm_backward,
@@ -402,3 +412,4 @@ from .layer_ops import (  # noqa: E402
     route_topk,
     route_topk_backward,
 )
+from .linear import linear_act, linear_act_backward  # noqa: E402

@@ -61,7 +61,7 @@ from .swiglu import (  # noqa: F401
     swiglu_values,
     swiglu_values_exact,
 )
-from . import layer_ops  # noqa: F401
+from . import layer_ops, products  # noqa: F401
 from .grouped_gemm import (  # noqa: F401
     MX_BLOCK,
     SCALE_K,
