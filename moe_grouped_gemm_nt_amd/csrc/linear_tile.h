@@ -16,7 +16,7 @@
 // 32 x 32 x 2 in float32 (lanes 0-31 hold the lower half of the step's K, lanes 32-63 the
 // upper; both operands number K alike). Turned bfloat16 operands are read by the LDS's
 // transposing reads, four k of one row a lane. W's rows are the instruction's first operand, its
-// rows permuted so that a lane ends up with 16 consecutive n of one m.
+// rows permuted so that a lane ends up with runs of 8 consecutive n of one m.
 #pragma once
 
 #include "gemm_engine.h"
@@ -63,42 +63,58 @@ struct TileForm {
 };
 
 // Row of a 32-row block that row i of the instruction's first operand is: its results, rows
-// 8 t + 4 g + e of the lanes of half g, are then columns 16 g + 4 t + e of the block.
+// 8 t + 4 g + e in register 4 t + e of the lanes of half g, are then columns
+// 16 (t / 2) + 8 g + 4 (t % 2) + e of the block.
 __device__ __forceinline__ int first_operand_row(int i) {
-  return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3);
+  return 16 * (i >> 4) + 8 * ((i >> 2) & 1) + 4 * ((i >> 3) & 1) + (i & 3);
 }
 
-// A copy's lane: where it reads, from the operand's first row of the tile and k = 0 of the slice.
+// A lane's part in an operand's copies. A wave's q-th copy of a slice is the KB q * WAVES + wave of
+// the operand's stage; from one of a lane's pieces to the next is a fixed distance, the same for
+// all lanes, so that one offset serves them all.
+template <class T, bool TURN, bool PAIRS, int ROWS>
 struct CopyLane {
-  uint32_t off;  // kOOB: no such row
-  int k;         // bytes of K before it (long), k before it (turned)
-};
-
-// Lane of the u-th KB of an operand of ROWS rows. `row_of` maps a tile's row to the operand's
-// row from the tile's first (or a negative number for none).
-template <class T, bool TURN, int ROWS, class RowOf>
-__device__ __forceinline__ CopyLane copy_lane(const Side& s, int u, int lane, RowOf row_of) {
-  CopyLane c;
-  if constexpr (!TURN) {
-    constexpr int PIECES = T::SLICE / 16;
-    const int row = u * (64 / PIECES) + lane / PIECES;
-    const int sw = T::SLICE == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
-    c.k = ((lane % PIECES) ^ sw) * 16;
-    const int r = row_of(row);
-    c.off = r < 0 ? mgg::kOOB : (uint32_t)(r * s.ld + c.k);
-  } else {
-    constexpr int RB = ROWS * T::ELEM;  // bytes of one k
-    const int at = u * 1024 + lane * 16;
-    const int k = at / RB;
-    int b = at % RB;
-    if constexpr (T::F32) b ^= ((k >> 2) & 1 & (RB / 128 - 1)) << 7;
-    else b ^= (k & 3 & (RB / 64 - 1)) << 6;
-    c.k = k;
-    const int r = row_of(b / T::ELEM);
-    c.off = r < 0 ? mgg::kOOB : (uint32_t)(k * s.ld + (int64_t)r * T::ELEM);
+  // rows (long) or k (turned) from one copy of a wave to its next
+  static constexpr int FURTHER = TURN ? T::WAVES * 1024 / (ROWS * T::ELEM) : T::WAVES * 1024 / T::SLICE;
+  static_assert(!TURN || FURTHER % (T::F32 ? 8 : 4) == 0, "pieces change places alike in all copies");
+  static_assert(TURN || FURTHER % (T::SLICE == 128 ? 16 : 4) == 0, "as above");
+  // PAIRS: 32 rows of one matrix, then 32 of the other. A KB is of one of them; which one goes by
+  // the wave (a round of copies has 64 rows) or by the copy (32 rows).
+  static constexpr bool BY_WAVE = FURTHER == 64;
+  static_assert(!PAIRS || FURTHER == 64 || FURTHER == 32, "whole blocks of 32 rows");
+  static constexpr int shared(int q) {  // rows or k before copy q
+    return !PAIRS ? q * FURTHER : BY_WAVE ? q * 32 : q / 2 * 32;
   }
-  return c;
-}
+  uint32_t off;  // of its first piece, from the tile's first row and the slice's first k
+  int at;        // row (long) or k (turned) of its first piece
+  int other;     // its bytes of K (long) or its row (turned)
+
+  __device__ __forceinline__ CopyLane(int64_t ld, int wave, int lane) {
+    if constexpr (!TURN) {
+      constexpr int PIECES = T::SLICE / 16;
+      const int row = wave * (64 / PIECES) + lane / PIECES;
+      const int sw = T::SLICE == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+      other = ((lane % PIECES) ^ sw) * 16;
+      at = PAIRS ? row % 32 : row;
+      off = (uint32_t)(at * ld + other);
+    } else {
+      constexpr int RB = ROWS * T::ELEM;  // bytes of one k
+      const int k = (wave * 1024 + lane * 16) / RB;
+      int b = (wave * 1024 + lane * 16) % RB;
+      if constexpr (T::F32) b ^= ((k >> 2) & 1 & (RB / 128 - 1)) << 7;
+      else b ^= (k & 3 & (RB / 64 - 1)) << 6;
+      other = b / T::ELEM;
+      at = k;
+      off = (uint32_t)(k * ld + b);
+    }
+  }
+  // Offset of the lane's piece of copy q, less that of the shared(q) rows or k.
+  __device__ __forceinline__ uint32_t offset(int q, int rows, int left) const {
+    const bool there = TURN ? at < left - shared(q) && other < rows
+                            : at < rows - shared(q) && other < left;
+    return there ? off : mgg::kOOB;
+  }
+};
 
 // Fragments of one step: 16 bytes a lane for each 32 rows.
 typedef uint4 Frag;
@@ -119,7 +135,7 @@ struct FragReader {
     } else {
       constexpr int RB = ROWS * 2;
       const int kk = (lane & 15) >> 2, quad = 4 * ((lane >> 4) & 1) + (lane & 3);
-      const int col = FIRST ? 16 * (quad & 1) + 4 * (quad >> 1) : 4 * quad;
+      const int col = FIRST ? first_operand_row(4 * quad) : 4 * quad;
       base = (8 * (lane >> 5) + kk) * RB + (((part >> 5) ^ (kk & (RB / 64 - 1))) << 6) + col * 2;
     }
   }
@@ -162,41 +178,60 @@ __device__ __forceinline__ v16f multiply(const Frag& w, const Frag& x, v16f acc)
   }
 }
 
-// acc = the tile's sums over K elements from k0 on, `k_len` of them (any number, also none). x and
-// w stand at the tile's first row (long) or column (turned) and at k0, and have `rows` rows from
-// there on; PAIRS: so does the second matrix, `second` bytes behind w.
+// Slices of a tile: one at least, so that a sum of nothing is a tile like others.
 template <class T>
-__device__ __forceinline__ void tile_sums(const Side& x, const Side& w, int64_t second, int k_len,
-                                          uint8_t* lds, v16f (&acc)[T::RI][T::RJ]) {
+__device__ __forceinline__ int slices_of(int k_len) {
+  return max(1, (k_len - 1) / T::SLICE_K + 1);
+}
+
+// Where a tile's operands start and what is left of them: x and w stand at the tile's first row
+// (long) or column (turned) and at its first k, and have `rows` rows from there on; PAIRS: so does
+// the second matrix of w, `second` bytes behind it.
+struct TileAt {
+  const uint8_t *x, *w;
+  int rows_x, rows_w, k_len;
+};
+
+// The tiles of a workgroup one after another. `at(n, TileAt&)` tells where its n-th tile is, or
+// returns false behind the last; `done(n, acc)` takes the tile's sums. Slices of all tiles are one
+// stream: a tile's first ones are on their way while the tile before is finished and handed over.
+template <class T, class At, class Done>
+__device__ __forceinline__ void tile_stream(const Side& x, const Side& w, int64_t second,
+                                            uint8_t* lds, At at, Done done) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const auto x_row = [&](int r) { return r < x.rows ? r : -1; };
-  const auto w_row = [&](int r) {
-    if constexpr (T::PAIRS) r = (r >> 6) * 32 + (r & 31);
-    return r < w.rows ? r : -1;
-  };
-  CopyLane cx[T::X_COPIES], cw[T::W_COPIES];
-#pragma unroll
-  for (int q = 0; q < T::X_COPIES; ++q)
-    cx[q] = copy_lane<T, T::TURN_X, T::BM>(x, q * T::WAVES + wave, lane, x_row);
-#pragma unroll
-  for (int q = 0; q < T::W_COPIES; ++q)
-    cw[q] = copy_lane<T, T::TURN_W, T::BN>(w, q * T::WAVES + wave, lane, w_row);
-
   const uint32_t lds0 = mgg::lds_addr(lds) + wave * 1024;
-  const int slices = (k_len + T::SLICE_K - 1) / T::SLICE_K;
-  // Copies go slice by slice. Those past the last slice read nothing and write zeros, so that the
-  // number of copies under way is the same in every slice.
-  int left_x = T::TURN_X ? k_len : k_len * T::ELEM, left_w = T::TURN_W ? k_len : k_len * T::ELEM;
-  const uint8_t *px = x.p, *pw = w.p;
-  v4i rx, rw, rw2;
+
+  // ---- copies: the tile that they are at, and the slice of it
+  const CopyLane<T, T::TURN_X, false, T::BM> cx(x.ld, wave, lane);
+  const CopyLane<T, T::TURN_W, T::PAIRS, T::BN> cw(w.ld, wave, lane);
+  const uint8_t *px, *pw;
+  int left_x, left_w;       // of K: bytes (long) or elements (turned)
+  int rows_x, rows_w;
+  int copy_tile = 0, copy_left;  // slices of that tile to come
   int to_stage = 0;
+  v4i rx, rw, rw2;
+  auto begin_tile = [&]() {
+    TileAt t;
+    if (!at(copy_tile, t)) {
+      // behind the last tile nothing is read, zeros are written: the number of copies under way
+      // is the same in every slice
+      t.x = x.p, t.w = w.p;
+      t.rows_x = t.rows_w = 0;
+      t.k_len = INT32_MAX / 8;
+    }
+    px = t.x, pw = t.w;
+    rows_x = t.rows_x, rows_w = t.rows_w;
+    left_x = T::TURN_X ? t.k_len : t.k_len * T::ELEM;
+    left_w = T::TURN_W ? t.k_len : t.k_len * T::ELEM;
+    copy_left = slices_of<T>(t.k_len);
+  };
   auto begin_slice = [&]() {
     rx = mgg::make_rsrc(px, 0x7fffffffu);
-    rw = mgg::make_rsrc(pw, 0x7fffffffu);
+    rw = mgg::make_rsrc(pw + (T::PAIRS && cw.BY_WAVE && wave >= 4 ? second : 0), 0x7fffffffu);
     mgg::pin_sgpr(rx);
     mgg::pin_sgpr(rw);
-    if constexpr (T::PAIRS) {
+    if constexpr (T::PAIRS && !cw.BY_WAVE) {
       rw2 = mgg::make_rsrc(pw + second, 0x7fffffffu);
       mgg::pin_sgpr(rw2);
     }
@@ -204,40 +239,29 @@ __device__ __forceinline__ void tile_sums(const Side& x, const Side& w, int64_t 
   };
   auto copy = [&](int q) {  // the q-th of COPIES
     if (q < T::X_COPIES) {
-      const CopyLane& c = cx[q < T::X_COPIES ? q : 0];
-      const uint32_t off = c.k < left_x ? c.off : mgg::kOOB;
-      mgg::dma_x4(lds0 + to_stage * T::STAGE + q * T::WAVES * 1024, rx, off);
+      mgg::dma_x4_so(lds0 + to_stage * T::STAGE + q * T::WAVES * 1024, rx,
+                     cx.offset(q, rows_x, left_x), (uint32_t)(cx.shared(q) * x.ld));
     } else {
       const int qw = q - T::X_COPIES;
-      const CopyLane& c = cw[qw >= 0 && qw < T::W_COPIES ? qw : 0];
-      const uint32_t off = c.k < left_w ? c.off : mgg::kOOB;
-      const uint32_t at = lds0 + to_stage * T::STAGE + T::X_BYTES + qw * T::WAVES * 1024;
-      if constexpr (T::PAIRS) {
-        // the KB's rows are all of one matrix
-        const bool up = ((qw * T::WAVES + wave) * (1024 / T::SLICE) >> 5) & 1;
-        if (up) mgg::dma_x4(at, rw2, off);
-        else mgg::dma_x4(at, rw, off);
-      } else {
-        mgg::dma_x4(at, rw, off);
-      }
+      mgg::dma_x4_so(lds0 + to_stage * T::STAGE + T::X_BYTES + qw * T::WAVES * 1024,
+                     T::PAIRS && !cw.BY_WAVE && qw % 2 ? rw2 : rw,
+                     cw.offset(qw, rows_w, left_w), (uint32_t)(cw.shared(qw) * w.ld));
     }
   };
   auto end_slice = [&]() {
-    px += T::TURN_X ? T::SLICE_K * x.ld : T::SLICE;
-    pw += T::TURN_W ? T::SLICE_K * w.ld : T::SLICE;
-    left_x -= T::TURN_X ? T::SLICE_K : T::SLICE;
-    left_w -= T::TURN_W ? T::SLICE_K : T::SLICE;
     to_stage = to_stage + 1 == T::S ? 0 : to_stage + 1;
+    if (--copy_left == 0) {
+      ++copy_tile;
+      begin_tile();
+    } else {
+      px += T::TURN_X ? T::SLICE_K * x.ld : T::SLICE;
+      pw += T::TURN_W ? T::SLICE_K * w.ld : T::SLICE;
+      left_x -= T::TURN_X ? T::SLICE_K : T::SLICE;
+      left_w -= T::TURN_W ? T::SLICE_K : T::SLICE;
+    }
   };
 
-#pragma unroll
-  for (int i = 0; i < T::RI; ++i)
-#pragma unroll
-    for (int j = 0; j < T::RJ; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-  if (slices <= 0) return;
-
+  // ---- products
   const int wi = wave / T::WJ * 32 * T::RI, wj = wave % T::WJ * 32 * T::RJ;
   const FragReader<T, T::TURN_X, false, T::BM> read_x(wi, lane);
   const FragReader<T, T::TURN_W, true, T::BN> read_w(wj, lane);
@@ -250,7 +274,6 @@ __device__ __forceinline__ void tile_sums(const Side& x, const Side& w, int64_t 
     if (n < T::RJ) f.w[n < T::RJ ? n : 0] = read_w.read(base + T::X_BYTES, n, step);
     else f.x[n < T::RJ ? 0 : n - T::RJ] = read_x.read(base, n - T::RJ, step);
   };
-
   // The copies of a slice are dealt to WINDOW steps: the last step of the slice S before it, whose
   // stage it takes, and the ones after that.
   constexpr int WINDOW = T::STEPS < T::WINDOW ? T::STEPS : T::WINDOW;
@@ -259,6 +282,8 @@ __device__ __forceinline__ void tile_sums(const Side& x, const Side& w, int64_t 
     for (int q = 0; q < T::COPIES; ++q)
       if (q * WINDOW * T::RI / T::COPIES == pos * T::RI + i) copy(q);
   };
+
+  begin_tile();
   for (int s = 0; s < T::S - 1; ++s) {
     begin_slice();
 #pragma unroll
@@ -274,36 +299,47 @@ __device__ __forceinline__ void tile_sums(const Side& x, const Side& w, int64_t 
 #pragma unroll
   for (int n = 0; n < READS; ++n) read(now, n, 0, 0);
   int stage = 0;
-  for (int s = 0; s < slices; ++s) {
-    const int then = stage + 1 == T::S ? 0 : stage + 1;
+  TileAt t;
+  for (int tile = 0; at(tile, t); ++tile) {
+    v16f acc[T::RI][T::RJ];
 #pragma unroll
-    for (int step = 0; step < T::STEPS; ++step) {
-      const bool last = step == T::STEPS - 1;
-      if (last) {
-        // The next slice has landed, and everyone has read this one to its end.
-        end_slice();
-        mgg::vm_wait_imm<(T::S - 2) * T::COPIES>();
-        mgg::lds_barrier();
-        begin_slice();
+    for (int i = 0; i < T::RI; ++i)
+#pragma unroll
+      for (int j = 0; j < T::RJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    const int slices = slices_of<T>(t.k_len);
+    for (int s = 0; s < slices; ++s) {
+      const int then = stage + 1 == T::S ? 0 : stage + 1;
+#pragma unroll
+      for (int step = 0; step < T::STEPS; ++step) {
+        const bool last = step == T::STEPS - 1;
+        if (last) {
+          // The next slice has landed, and everyone has read this one to its end.
+          end_slice();
+          mgg::vm_wait_imm<(T::S - 2) * T::COPIES>();
+          mgg::lds_barrier();
+          begin_slice();
+        }
+#pragma unroll
+        for (int i = 0; i < T::RI; ++i) {
+#pragma unroll
+          for (int j = 0; j < T::RJ; ++j)
+            acc[i][j] = multiply<T::F32>(now.w[j], now.x[i], acc[i][j]);
+#pragma unroll
+          for (int n = 0; n < READS; ++n)
+            if (n * T::RI / READS == i) read(next, n, last ? then : stage, last ? 0 : step + 1);
+          if (last) copies(0, i);
+          else if (step + 1 < WINDOW) copies(step + 1, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        now = next;
       }
-#pragma unroll
-      for (int i = 0; i < T::RI; ++i) {
-#pragma unroll
-        for (int j = 0; j < T::RJ; ++j)
-          acc[i][j] = multiply<T::F32>(now.w[j], now.x[i], acc[i][j]);
-#pragma unroll
-        for (int n = 0; n < READS; ++n)
-          if (n * T::RI / READS == i) read(next, n, last ? then : stage, last ? 0 : step + 1);
-        if (last) copies(0, i);
-        else if (step + 1 < WINDOW) copies(step + 1, i);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      now = next;
+      stage = then;
     }
-    stage = then;
+    done(tile, acc);
   }
-  mgg::vm_wait_imm<0>();
-  mgg::lds_barrier();  // LDS is free, nothing is on its way into it
+  mgg::vm_wait_imm<0>();  // nothing is on its way into LDS when the workgroup ends
 }
 
 }  // namespace mgg_dense

@@ -103,6 +103,59 @@ def test_forward_sizes(dtype, M, N, K):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(130, 258, 2056), (300, 70, 5000), (90, 40, 3333), (70, 3000, 640)])
+def test_long_sums(dtype, M, N, K):
+    """Few tiles and a long axis, which is cut into parts: of x w^T, and, with the sides exchanged,
+    of dz w and dz^T x."""
+    print(dtype, M, N, K, flush=True)
+    x, w = make((M, K), dtype, 90), make((N, K), dtype, 91, K ** -0.5)
+    check_forward(x, w, make((N,), F32, 92), "silu", make((M, N), F32, 93), F32)
+    check_forward(x, w, None, "swiglu")
+    for m, n, k in ((M, K, N), (K, M, N)):
+        x, w = make((m, k), dtype, 94), make((n, k), dtype, 95)
+        check_backward(x, w, make((m, n), dtype, 96), make((m, n), dtype, 97), "relu")
+
+
+@pytest.mark.parametrize("M,N,K", [(4100, 4104, 72), (4352, 4096, 64), (4200, 4360, 136)])
+def test_large_tiles(M, N, K):
+    """As many rows and columns as fill the GPU with the largest tiles, with and without some left
+    over; outputs in pieces and not. Against float64 on the GPU."""
+    print(M, N, K, flush=True)
+    x, w, b = make((M, K), BF, 100), make((N, K), BF, 101, K ** -0.5), make((N,), BF, 102)
+    X, W = x.double(), w.double()
+    z = X @ W.t() + b.double()
+    err = (K + 10) * U * (X.abs() @ W.abs().t() + b.double().abs())
+    for func, cols in (("none", N), ("swiglu", N // 2), ("gelu", N)):
+        for out, ld in ((BF, cols), (F32, cols), (BF, cols + 1)):
+            r = make((M, ld), out, 103)[:, :cols]
+            got, gz = mgg.linear_act(x, w, b, func, r, keep_z=True, out_dtype=out)
+            if func == "swiglu":
+                g, u = z.chunk(2, 1)
+                eg, eu = err.chunk(2, 1)
+                h = g * torch.sigmoid(g)
+                want, e = h * u, 1.1 * eg * u.abs() + h.abs() * eu + (16 + 2 * g.abs()) * U * (h * u).abs()
+            else:
+                want = z if func == "none" else torch.nn.functional.gelu(z)
+                e = 1.13 * err + (16 + 2 * z.abs()) * U * want.abs()
+            want = want + r.double()
+            e = e + U * r.double().abs() + half_step(out) * want.abs()
+            assert ((got.double() - want).abs() <= e).all()
+            assert ((gz.double() - z).abs() <= err + half_step(BF) * z.abs()).all()
+    # the same sizes as the sides of the gradients: dz [k, m] gives d_w [m, n], dz [m, k] d_x [m, n]
+    for rows, d, other, turned in ((K, make((K, M), BF, 104), make((K, N), BF, 105), True),
+                                   (M, make((M, K), BF, 106), make((K, N), BF, 107), False)):
+        if turned:
+            got = mgg.linear_act_backward(other, make((M, N), BF, 108), d, need_x=False)[1]
+            a, c = d.double().t(), other.double()
+        else:
+            got = mgg.linear_act_backward(make((M, N), BF, 109), other, d, need_w=False)[0]
+            a, c = d.double(), other.double()
+        want = a @ c
+        e = (K + 8) * U * (a.abs() @ c.abs()) + half_step(BF) * want.abs()
+        assert ((got.double() - want).abs() <= e).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("func", FUNCS)
 @pytest.mark.parametrize("M", [20, 150])
 def test_forward_functions(dtype, func, M):
