@@ -23,12 +23,13 @@ typedef enum { MGG_WEIGHT_BF16 = 0, MGG_WEIGHT_FP8 = 1, MGG_WEIGHT_FP4 = 2 } mgg
  *   out[t]  = residual[t] + sum_j weights[t, j] * W2[e] (silu(g) * u)
  * Other ids are skipped (route_topk's -1: whatever weight stands there has no effect); a token
  * that names no expert gets its residual, or 0. An expert named twice by a token counts with the
- * sum of its weights. Weights are dequantized, activations are not quantized; sums are float32,
- * silu(g) * u is held as two bfloat16 (16 significant bits) between the products.
+ * sum of its weights. Weights are dequantized, activations are not quantized; sums are float32.
+ * Between the products silu(g) * u is held as bfloat16 where the output is bfloat16, as between
+ * the grouped products, and as two of them (16 significant bits) where it is float32.
  *
- *   T, k, G     0 <= T <= 256; 1 <= k <= 32; 1 <= G <= 4096. The time goes with the experts
- *               that are named, each of which is read once for every 64 tokens that name it.
- *   H, I        1 <= H, I <= 2^17, multiples of 8 (bfloat16 weights) or of 128 (FP8, FP4).
+ *   T, k, G     0 <= T <= 128; 1 <= k <= 32; 1 <= G <= 4096. The time goes with the experts
+ *               that are named.
+ *   H, I        1 <= H, I <= 2^16, multiples of 8 (bfloat16 weights) or of 128 (FP8, FP4).
  *   x           bfloat16, [T] rows of H (ldx >= H).
  *   ids         int32 [T][k]; weights float32 [T][k].
  *   W13, W2     [G][2I][H] and [G][H][I] (FP4: half as many bytes a row), 16-byte aligned.

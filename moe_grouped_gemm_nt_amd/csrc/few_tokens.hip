@@ -5,8 +5,8 @@
 // as experts, and else the expert of place s, if no earlier place names it (a place is one of a
 // token's k choices). Which tokens name it, each workgroup finds by itself from the ids, so
 // nothing is sorted beforehand.
-//   few_up     h = silu(g) u of 8 columns for all of a slot's tokens: a workgroup holds 8 gate
-//              rows and their 8 up rows, its waves share K;
+//   few_up     h = silu(g) u of some columns for all of a slot's tokens: a wave multiplies 8 gate
+//              rows and their 8 up rows over a part of K, the slot's rows of x are in LDS;
 //   few_down   16 columns of the output for all tokens: a workgroup goes through every slot, its
 //              waves share the slots' K evenly, each with sums of its own for all tokens, which
 //              are added in a fixed order at the end.
@@ -20,9 +20,9 @@ namespace {
 using namespace mgg_layer;
 
 constexpr int kWaves = 8, kFewThreads = 64 * kWaves;
-constexpr int kMaxTokens = 256, kMaxPlaces = 32, kMaxExperts = 4096, kMaxWidth = 1 << 17;
-constexpr int kRowTiles = 4;   // token rows that a wave holds at once, in sixteens
+constexpr int kMaxTokens = 128, kMaxPlaces = 32, kMaxExperts = 4096, kMaxWidth = 1 << 16;
 constexpr int kUpColumns = 8, kDownColumns = 16;
+constexpr int kLdsBytes = 160 * 1024;
 constexpr int kPartLd = 20;    // words from one token's 16 sums to the next: 16-byte aligned
 
 struct FewArgs {
@@ -34,9 +34,10 @@ struct FewArgs {
   const uint8_t *w13, *w2;
   const void *s13, *s2;
   int2* slot_meta;       // [slots]: tokens, expert
-  int32_t* slot_rows;    // [slots][T]: the place of each token that names the expert
-  float* place_weight;   // [places]: what that token's output takes of the expert
-  uint16_t *h, *h_low;   // [places][I]: silu(g) u as two bfloat16
+  int2* slot_rows;       // [slots][T]: for each token that names the expert its place (low 16 bits)
+                         // and number, and what its output takes of the expert (float32 bits)
+  uint16_t *h, *h_low;   // [places][I]: silu(g) u as one bfloat16 or two
+  int x_rows;            // few_up: rows of x in LDS at a time
   mgg_act out_dt;
   const void* residual;
   int64_t ld_res;
@@ -50,20 +51,30 @@ __device__ int find_rows(const FewArgs& a, int slot, int& expert, int32_t* list)
   expert = a.by_expert ? slot : a.ids[slot];
   if (expert < 0 || expert >= a.G) return 0;
   int count = 0, last = -1;  // last: the token of the latest hit
-  for (int c = 0; c < a.places; c += 64) {
-    const int p = c + lane;
-    const bool hit = p < a.places && a.ids[p] == expert;
-    const uint64_t hits = __ballot(hit);
-    if (hits == 0) continue;
-    if (!a.by_expert && last < 0 && c + __builtin_ctzll(hits) != slot) return 0;
-    // a token's places stand together: only its first one counts
-    const uint64_t below = hits & ((1ull << lane) - 1);
-    const int before = below ? (c + 63 - __builtin_clzll(below)) / a.k : last;
-    const bool first = hit && p / a.k != before;
-    const uint64_t firsts = __ballot(first);
-    if (first) list[count + __popcll(firsts & ((1ull << lane) - 1))] = p;
-    count += __popcll(firsts);
-    last = (c + 63 - __builtin_clzll(hits)) / a.k;
+  constexpr int AT_ONCE = 8;
+  for (int c0 = 0; c0 < a.places; c0 += 64 * AT_ONCE) {
+    int id[AT_ONCE];
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int p = c0 + 64 * i + lane;
+      id[i] = p < a.places ? a.ids[p] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < AT_ONCE; ++i) {
+      const int c = c0 + 64 * i, p = c + lane;
+      const bool hit = id[i] == expert;
+      const uint64_t hits = __ballot(hit);
+      if (hits == 0) continue;
+      if (!a.by_expert && last < 0 && c + __builtin_ctzll(hits) != slot) return 0;
+      // a token's places stand together: only its first one counts
+      const uint64_t below = hits & ((1ull << lane) - 1);
+      const int before = below ? (c + 63 - __builtin_clzll(below)) / a.k : last;
+      const bool first = hit && p / a.k != before;
+      const uint64_t firsts = __ballot(first);
+      if (first) list[count + __popcll(firsts & ((1ull << lane) - 1))] = p;
+      count += __popcll(firsts);
+      last = (c + 63 - __builtin_clzll(hits)) / a.k;
+    }
   }
   wave_order();
   return count;
@@ -98,174 +109,226 @@ __device__ __forceinline__ float silu(float g) {
   return g * q;
 }
 
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT>
-__device__ __forceinline__ void up_rows(const FewArgs& a, int expert, int tile,
-                                        const int32_t* list, int count, float* s_part) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
-  const int i0 = tile * kUpColumns;
-  StreamRows<RT> rows;
-  const int n = (r < 8 ? 0 : a.I) + i0 + (r & 7);  // I is a multiple of 8
-  rows.w = a.w13 + ((int64_t)expert * 2 * a.I + n) * row_bytes<W>(a.H) + q * Form<W>::RUN_BYTES;
-  // FP8 scales multiply results, rows 4 q .. 4 q + 3 here; FP4 scales the lane's weights
-  const int ns = W == kFp4Weights ? n : (q < 2 ? 0 : a.I) + i0 + 4 * (q & 1);
-  set_scale<W, SF, SPAN>(a.s13, expert, 2 * a.I, a.H, ns, q, rows.scale, rows.scale_step);
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int at = 16 * t + r;
-    rows.x[t] = at < count ? reinterpret_cast<const uint8_t*>(a.x + (list[at] / a.k) * a.ldx) +
-                                 q * Form<W>::X_BYTES
-                           : nullptr;
-  }
-  v4f acc[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int blocks = cdiv(a.H, Form<W>::BLOCK);
-  stream_rows<W, SF, SPAN, RT, false>(rows, blocks * wave / kWaves, blocks * (wave + 1) / kWaves,
-                                      a.H, acc);
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-    *reinterpret_cast<v4f*>(s_part + ((wave * RT + t) * 16 + r) * kPartLd + 4 * q) = acc[t];
-  __syncthreads();
-  for (int i = threadIdx.x; i < RT * 16 * kUpColumns; i += kFewThreads) {
-    const int row = i / kUpColumns, c = i % kUpColumns;
-    if (row >= count) break;
-    float g = 0.f, u = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float* s = s_part + (w * RT * 16 + row) * kPartLd + c;
-      g += s[0];
-      u += s[8];
-    }
-    const float h = silu(g) * u;
-    const uint16_t hi = bf16_bits(h);
-    const float high = to_f32(bf16_t{hi});
-    const int64_t at = (int64_t)list[row] * a.I + i0 + c;
-    a.h[at] = hi;
-    a.h_low[at] = fabsf(high) < INFINITY ? bf16_bits(h - high) : 0;
-  }
+// A token row in LDS: whole blocks of K, and 16 bytes more so that rows start in different banks.
+template <WeightForm W>
+__host__ __device__ constexpr int x_row_bytes(int H) {
+  return cdiv(H, Form<W>::BLOCK) * Form<W>::BLOCK * 2 + 16;
 }
 
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
-__global__ __launch_bounds__(kFewThreads) void few_up(FewArgs a) {
+// AHEAD blocks of weights are on their way: 16 waves to a CU with 2 KB each (FP8).
+constexpr int kUpAhead = 4;
+
+// TILES: 8-column tiles of a workgroup, which shares K among kWaves / TILES waves for each. More
+// tiles mean fewer copies of x into LDS and longer streams, fewer workgroups.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int TILES>
+__global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
+  using F = Form<W>;
+  constexpr int PARTS = kWaves / TILES;
   extern __shared__ __align__(16) float s_few[];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tile = blockIdx.x, slot = blockIdx.y;
-  int32_t* list = reinterpret_cast<int32_t*>(s_few) + wave * a.T;
-  float* s_part = s_few + round_up(kWaves * a.T, 4);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
+  const int slot = blockIdx.y, tile = blockIdx.x * TILES + wave % TILES, part = wave / TILES;
+  const int x_ld = x_row_bytes<W>(a.H);
+  uint8_t* s_x = reinterpret_cast<uint8_t*>(s_few);
+  float* s_part = reinterpret_cast<float*>(s_x + a.x_rows * x_ld);
+  int32_t* list = reinterpret_cast<int32_t*>(s_part + kWaves * 16 * kPartLd) + wave * a.T;
   int expert;
   const int count = find_rows(a, slot, expert, list);
-  if (tile == 0 && threadIdx.x == 0) a.slot_meta[slot] = make_int2(count, expert);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.slot_meta[slot] = make_int2(count, expert);
   if (count == 0) return;
-  if (tile == 0) {
+
+  const int i0 = tile * kUpColumns;
+  const bool live = i0 < a.I;  // a wave behind the last column has nothing to multiply
+  const int n = live ? (r < 8 ? 0 : a.I) + i0 + (r & 7) : 0;  // I is a multiple of 8
+  const uint8_t* w = a.w13 + ((int64_t)expert * 2 * a.I + n) * row_bytes<W>(a.H) + q * F::RUN_BYTES;
+  // FP8 scales multiply results, rows 4 q .. 4 q + 3 here; FP4 scales the lane's weights
+  const int ns = W == kFp4Weights ? n : live ? (q < 2 ? 0 : a.I) + i0 + 4 * (q & 1) : 0;
+  const void* scale;
+  int64_t scale_step;
+  set_scale<W, SF, SPAN>(a.s13, expert, 2 * a.I, a.H, ns, q, scale, scale_step);
+  const int blocks = cdiv(a.H, F::BLOCK);
+  const int from = blocks * part / PARTS, to = live ? blocks * (part + 1) / PARTS : from;
+
+  for (int r0 = 0; r0 < count; r0 += a.x_rows) {
+    const int rows = min(a.x_rows, count - r0);
+    WeightBlock<W, SF, SPAN> ring[kUpAhead];
+#pragma unroll
+    for (int i = 0; i < kUpAhead; ++i)
+      if (from + i < to) load_weights<W, SF, SPAN>(ring[i], w, scale, scale_step, from + i, a.H);
+    if (r0 > 0) __syncthreads();  // everyone is done with the rows and sums before
+    const int pieces = (x_ld - 16) / 16;
+    for (int row = 0; row < rows; row += 4) {
+      const uint16_t* from_x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        from_x[i] = a.x + (int64_t)(list[r0 + min(row + i, rows - 1)] / a.k) * a.ldx;
+      for (int c = threadIdx.x; c < pieces; c += kFewThreads) {
+        const int left = (a.H - 8 * c) * 2;
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = left >= 16 ? load16(from_x[i] + 8 * c) : load16_part<2>(from_x[i] + 8 * c, left);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (row + i < rows) *reinterpret_cast<uint4*>(s_x + (row + i) * x_ld + c * 16) = v[i];
+      }
+    }
+    __syncthreads();
+    v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
+    // lanes without a row repeat the first one; nobody reads their results
+    const uint8_t* xr = s_x + (r < rows ? r : 0) * x_ld + q * F::X_BYTES;
+    for (int b = from; b < to; b += kUpAhead)
+#pragma unroll
+      for (int i = 0; i < kUpAhead; ++i)
+        if (b + i < to) {
+          const uint8_t* xb = xr + (b + i) * (4 * F::X_BYTES);
+          auto x = [&](int, int j) { return *reinterpret_cast<const uint4*>(xb + 16 * j); };
+          multiply_block<W, SF, SPAN, 1, false>(ring[i], acc, x, x);
+          if (b + i + kUpAhead < to)
+            load_weights<W, SF, SPAN>(ring[i], w, scale, scale_step, b + i + kUpAhead, a.H);
+        }
+    *reinterpret_cast<v4f*>(s_part + (wave * 16 + r) * kPartLd + 4 * q) = acc[0];
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * TILES * kUpColumns; i += kFewThreads) {
+      const int row = i / (TILES * kUpColumns), t = i / kUpColumns % TILES, c = i % kUpColumns;
+      const int col = (blockIdx.x * TILES + t) * kUpColumns + c;
+      if (col >= a.I) continue;
+      float g = 0.f, u = 0.f;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const float* s = s_part + ((p * TILES + t) * 16 + row) * kPartLd + c;
+        g += s[0];
+        u += s[8];
+      }
+      const float h = silu(g) * u;
+      const uint16_t hi = bf16_bits(h);
+      const int64_t at = (int64_t)list[r0 + row] * a.I + col;
+      a.h[at] = hi;
+      if (a.out_dt == MGG_ACT_F32) {
+        const float high = to_f32(bf16_t{hi});
+        a.h_low[at] = fabsf(high) < INFINITY ? bf16_bits(h - high) : 0;
+      }
+    }
+  }
+  if (blockIdx.x == 0)  // what few_down needs to know of the slot
     for (int i = threadIdx.x; i < count; i += kFewThreads) {
-      const int p = list[i], end = (p / a.k + 1) * a.k;
+      const int p = list[i], t = p / a.k;
       float sum = 0.f;
-      for (int j = p; j < end; ++j)
+      for (int j = p; j < (t + 1) * a.k; ++j)
         if (a.ids[j] == expert) sum += a.weights[j];
-      a.slot_rows[(int64_t)slot * a.T + i] = p;
-      a.place_weight[p] = sum;
-    }
-  }
-  for (int r0 = 0; r0 < count; r0 += 16 * kRowTiles) {
-    const int left = count - r0;
-    if (r0 > 0) __syncthreads();  // everyone has read the sums before
-    if (left <= 16) up_rows<W, SF, SPAN, 1>(a, expert, tile, list + r0, left, s_part);
-    else if (left <= 32) up_rows<W, SF, SPAN, 2>(a, expert, tile, list + r0, left, s_part);
-    else up_rows<W, SF, SPAN, 4>(a, expert, tile, list + r0, left, s_part);
-  }
-}
-
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT>
-__device__ __forceinline__ void down_rows(const FewArgs& a, int expert, int n0,
-                                          const int32_t* list, int count, int from, int to,
-                                          float* sums) {
-  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  StreamRows<RT> rows;
-  const int n = min(n0 + r, a.H - 1);
-  rows.w = a.w2 + ((int64_t)expert * a.H + n) * row_bytes<W>(a.I) + q * Form<W>::RUN_BYTES;
-  const int ns = W == kFp4Weights ? n : min(n0 + 4 * q, a.H - 4);
-  set_scale<W, SF, SPAN>(a.s2, expert, a.H, a.I, ns, q, rows.scale, rows.scale_step);
-  int place[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    place[t] = 16 * t + r < count ? list[16 * t + r] : -1;
-    const int64_t at = ((int64_t)place[t] * a.I) * 2 + q * Form<W>::X_BYTES;
-    rows.x[t] = place[t] < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h) + at;
-    rows.x_low[t] = reinterpret_cast<const uint8_t*>(a.h_low) + at;
-  }
-  v4f acc[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
-  stream_rows<W, SF, SPAN, RT, true>(rows, from, to, a.I, acc);
-#pragma unroll
-  for (int t = 0; t < RT; ++t)
-    if (place[t] >= 0) {
-      const float weight = a.place_weight[place[t]];
-      v4f* s = reinterpret_cast<v4f*>(sums + (place[t] / a.k) * kDownColumns + 4 * q);
-      v4f v = *s;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = fmaf(weight, acc[t][e], v[e]);
-      *s = v;
+      a.slot_rows[(int64_t)slot * a.T + i] = make_int2(p | t << 16, __float_as_int(sum));
     }
 }
 
-// A slot with tokens in one word.
-__device__ __forceinline__ uint32_t pack_slot(int slot, int count, int expert) {
-  return (uint32_t)slot | (uint32_t)(count - 1) << 12 | (uint32_t)expert << 20;
+// A job of few_down is up to 16 tokens of a slot, in one word: the first of its rows in the list of
+// all slots' rows, their number less 1, and the expert.
+__device__ __forceinline__ uint32_t pack_job(int row, int count, int expert) {
+  return (uint32_t)row | (uint32_t)(count - 1) << 16 | (uint32_t)expert << 20;
 }
+constexpr int kMaxJobs(int slots, int places) { return slots + places / 16; }
 
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
-__global__ __launch_bounds__(kFewThreads) void few_down(FewArgs a) {
+// LOW: h is two bfloat16.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, bool LOW>
+__global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) {
+  using F = Form<W>;
+  constexpr int AHEAD = LOW ? 3 : W == kBf16Weights ? 4 : 3;
   extern __shared__ __align__(16) float s_few[];
-  __shared__ int s_count[kWaves];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ int2 s_total[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * kDownColumns;
   float* sums = s_few + wave * a.T * kDownColumns;
-  uint32_t* s_slots = reinterpret_cast<uint32_t*>(s_few + kWaves * a.T * kDownColumns);
+  int2* s_rows = reinterpret_cast<int2*>(s_few + kWaves * a.T * kDownColumns);
+  uint32_t* s_jobs = reinterpret_cast<uint32_t*>(s_rows + a.places);
   for (int i = lane; i < a.T * kDownColumns; i += 64) sums[i] = 0.f;
-  // the slots that have tokens, in order
-  int active = 0;
+  // the slots' rows one behind the other, and their jobs, in the order of the slots
+  int rows = 0, jobs = 0;
   for (int s0 = 0; s0 < a.slots; s0 += kFewThreads) {
     const int slot = s0 + threadIdx.x;
     const int2 meta = slot < a.slots ? a.slot_meta[slot] : make_int2(0, 0);
-    const uint64_t mask = __ballot(meta.x > 0);
-    if (lane == 0) s_count[wave] = __popcll(mask);
+    const int mine = cdiv(meta.x, 16);
+    int before_r = lanes_prefix<64>(meta.x), before_j = lanes_prefix<64>(mine);
+    if (lane == 63) s_total[wave] = make_int2(before_r, before_j);
     __syncthreads();
-    int at = active + __popcll(mask & ((1ull << lane) - 1));
+    before_r += rows - meta.x;
+    before_j += jobs - mine;
     for (int w = 0; w < kWaves; ++w) {
-      at += w < wave ? s_count[w] : 0;
-      active += s_count[w];
+      before_r += w < wave ? s_total[w].x : 0;
+      before_j += w < wave ? s_total[w].y : 0;
+      rows += s_total[w].x;
+      jobs += s_total[w].y;
     }
-    if (meta.x > 0) s_slots[at] = pack_slot(slot, meta.x, meta.y);
+    const int2* from = a.slot_rows + (int64_t)slot * a.T;
+#pragma unroll 4
+    for (int i = 0; i < meta.x; ++i) s_rows[before_r + i] = from[i];
+    for (int j = 0; j < mine; ++j)
+      s_jobs[before_j + j] = pack_job(before_r + 16 * j, min(16, meta.x - 16 * j), meta.y);
     __syncthreads();
   }
-  const int blocks = cdiv(a.I, Form<W>::BLOCK), units = active * blocks;
-  int u = (int)((int64_t)units * wave / kWaves);
+
+  const int blocks = cdiv(a.I, F::BLOCK);
+  const int units = jobs * blocks;
+  const int first = (int)((int64_t)units * wave / kWaves);
   const int end = (int)((int64_t)units * (wave + 1) / kWaves);
-  while (u < end) {
-    const int from = u % blocks, to = min(blocks, from + end - u);
-    const uint32_t packed = s_slots[u / blocks];
-    const int slot = packed & 4095, count = ((packed >> 12) & 255) + 1, expert = packed >> 20;
-    const int32_t* list = a.slot_rows + (int64_t)slot * a.T;
-    for (int r0 = 0; r0 < count; r0 += 16 * kRowTiles) {
-      const int left = count - r0;
-      if (left <= 16)
-        down_rows<W, SF, SPAN, 1>(a, expert, n0, list + r0, left, from, to, sums);
-      else if (left <= 32)
-        down_rows<W, SF, SPAN, 2>(a, expert, n0, list + r0, left, from, to, sums);
-      else
-        down_rows<W, SF, SPAN, 4>(a, expert, n0, list + r0, left, from, to, sums);
-    }
-    u += to - from;
-  }
+  const int n = min(n0 + r, a.H - 1), ns = W == kFp4Weights ? n : min(n0 + 4 * q, a.H - 4);
+  WeightBlock<W, SF, SPAN> weights[AHEAD];
+  TokenBlock<W, 1, LOW> tokens[AHEAD];
+  // the unit to load next: block `lb` of job `lj`
+  int lj = first / blocks, lb = first % blocks;
+  auto load = [&](int i) {
+    const uint32_t job = s_jobs[lj];
+    const int row = job & 0xffff, count = (job >> 16 & 15) + 1, expert = job >> 20;
+    const uint8_t* w = a.w2 + ((int64_t)expert * a.H + n) * row_bytes<W>(a.I) + q * F::RUN_BYTES;
+    const void* scale;
+    int64_t step;
+    set_scale<W, SF, SPAN>(a.s2, expert, a.H, a.I, ns, q, scale, step);
+    load_weights<W, SF, SPAN>(weights[i], w, scale, step, lb, a.I);
+    const int place = r < count ? s_rows[row + r].x & 0xffff : -1;
+    const int64_t at = (int64_t)place * a.I * 2 + q * F::X_BYTES;
+    load_tokens<W>(tokens[i].x[0], place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h) + at,
+                   lb, a.I);
+    if constexpr (LOW)
+      load_tokens<W>(tokens[i].x_low[0],
+                     place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h_low) + at, lb, a.I);
+    if (++lb == blocks) lb = 0, ++lj;
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (first + i < end) load(i);
+  v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
+  int job_at = first / blocks, block_at = first % blocks;
+  for (int u = first; u < end; u += AHEAD)
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (u + i < end) {
+        auto x = [&](int, int j) { return tokens[i].x[0][j]; };
+        auto x_low = [&](int, int j) { return tokens[i].x_low[0][j]; };
+        multiply_block<W, SF, SPAN, 1, LOW>(weights[i], acc, x, x_low);
+        if (u + i + AHEAD < end) load(i);
+        if (++block_at == blocks || u + i + 1 == end) {
+          // a wave's tokens of one job are different ones
+          const uint32_t job = s_jobs[job_at];
+          if (r < (int)(job >> 16 & 15) + 1) {
+            const int2 row = s_rows[(job & 0xffff) + r];
+            const float weight = __int_as_float(row.y);
+            v4f* s = reinterpret_cast<v4f*>(sums + (row.x >> 16) * kDownColumns + 4 * q);
+            v4f v = *s;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = fmaf(weight, acc[0][e], v[e]);
+            *s = v;
+          }
+          wave_order();
+          acc[0] = v4f{0.f, 0.f, 0.f, 0.f};
+          block_at = 0;
+          ++job_at;
+        }
+      }
   __syncthreads();
   for (int i = threadIdx.x; i < a.T * kDownColumns; i += kFewThreads) {
-    const int t = i / kDownColumns, n = n0 + i % kDownColumns;
-    if (n >= a.H) continue;
+    const int t = i / kDownColumns, col = n0 + i % kDownColumns;
+    if (col >= a.H) continue;
     float v = 0.f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) v += s_few[w * a.T * kDownColumns + i];
-    const int64_t at = (int64_t)t * a.H + n, res = t * a.ld_res + n;
+    const int64_t at = (int64_t)t * a.H + col, res = t * a.ld_res + col;
     if (a.out_dt == MGG_ACT_BF16) {
       if (a.residual) v += to_f32(reinterpret_cast<const bf16_t*>(a.residual)[res]);
       reinterpret_cast<bf16_t*>(a.out)[at] = from_f32<bf16_t>(v);
@@ -278,7 +341,7 @@ __global__ __launch_bounds__(kFewThreads) void few_down(FewArgs a) {
 
 // Where the workspace's parts start.
 struct FewWorkspace {
-  size_t meta, rows, weight, h, h_low, bytes;
+  size_t meta, rows, h, h_low, bytes;
   FewWorkspace(int T, int k, int G, int I) {
     const size_t places = (size_t)T * k, slots = std::min<size_t>(places, G);
     size_t at = 0;
@@ -288,8 +351,7 @@ struct FewWorkspace {
       return here;
     };
     meta = take(slots * sizeof(int2));
-    rows = take(slots * T * 4);
-    weight = take(places * 4);
+    rows = take(slots * T * sizeof(int2));
     h = take(places * I * 2);
     h_low = take(places * I * 2);
     bytes = at;
@@ -311,13 +373,37 @@ bool launch_few(F kernel, dim3 grid, size_t lds, const FewArgs& a, hipStream_t s
   return true;
 }
 
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int TILES>
+bool run_up(const FewArgs& a, hipStream_t stream) {
+  const size_t lds = (size_t)a.x_rows * x_row_bytes<W>(a.H) +
+                     ((size_t)kWaves * 16 * kPartLd + (size_t)kWaves * a.T) * 4;
+  return launch_few(few_up<W, SF, SPAN, TILES>,
+                    dim3(cdiv(cdiv(a.I, kUpColumns), TILES), a.slots), lds, a, stream);
+}
+
 template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
-bool run_few(const FewArgs& a, hipStream_t stream) {
-  const int tiles = std::min(kRowTiles, cdiv(a.T, 16)) == 3 ? 4 : std::min(kRowTiles, cdiv(a.T, 16));
-  const size_t up = (round_up(kWaves * a.T, 4) + (size_t)kWaves * tiles * 16 * kPartLd) * 4;
-  const size_t down = ((size_t)kWaves * a.T * kDownColumns + a.slots) * 4;
-  return launch_few(few_up<W, SF, SPAN>, dim3(cdiv(a.I, kUpColumns), a.slots), up, a, stream) &&
-         launch_few(few_down<W, SF, SPAN>, dim3(cdiv(a.H, kDownColumns)), down, a, stream);
+bool run_few(FewArgs a, hipStream_t stream) {
+  // Rows of x in LDS: what an expert can be expected to have twice over, in two workgroups to a
+  // CU where that leaves four rows, else in one.
+  const int mean = cdiv(a.places, a.G);
+  const int want = a.T <= 4 ? a.T : mean <= 2 ? 4 : mean <= 4 ? 8 : 16;
+  const int rest = (int)((size_t)kWaves * 16 * kPartLd + (size_t)kWaves * a.T) * 4;
+  const int row = x_row_bytes<W>(a.H);
+  const int half = (kLdsBytes / 2 - rest) / row, all = (kLdsBytes - rest) / row;
+  a.x_rows = std::min(std::min(want, 16), half >= 4 || half >= want ? std::max(half, 1) : all);
+  if (want > 8 && all >= 16) a.x_rows = 16;
+  // Tiles of a workgroup: as many as leave about three workgroups for each CU, and a block of K for
+  // each wave.
+  const int64_t tiles = (int64_t)cdiv(a.I, kUpColumns) * std::min(a.slots, a.places);
+  const int blocks = cdiv(a.H, Form<W>::BLOCK);
+  const bool up = tiles >= 4 * 768 || blocks < 4 ? run_up<W, SF, SPAN, 4>(a, stream)
+                  : tiles >= 2 * 768 || blocks < 8 ? run_up<W, SF, SPAN, 2>(a, stream)
+                                                   : run_up<W, SF, SPAN, 1>(a, stream);
+  const size_t lds = (size_t)kWaves * a.T * kDownColumns * 4 + a.places * sizeof(int2) +
+                     kMaxJobs(a.slots, a.places) * 4;
+  const dim3 grid(cdiv(a.H, kDownColumns));
+  return up && (a.out_dt == MGG_ACT_F32 ? launch_few(few_down<W, SF, SPAN, true>, grid, lds, a, stream)
+                                        : launch_few(few_down<W, SF, SPAN, false>, grid, lds, a, stream));
 }
 
 }  // namespace
@@ -338,12 +424,12 @@ mgg_status moe_few_tokens(mgg_weight wt, int T, int k, int G, int H, int I, cons
   if (wt != MGG_WEIGHT_BF16 && wt != MGG_WEIGHT_FP8 && wt != MGG_WEIGHT_FP4)
     return fail(MGG_EINVAL, "unknown weight type");
   if (!known(out_dt)) return fail(MGG_EINVAL, "unknown element type");
-  if (T < 0 || T > kMaxTokens) return fail(MGG_EINVAL, "T must be in [0, 256]");
+  if (T < 0 || T > kMaxTokens) return fail(MGG_EINVAL, "T must be in [0, 128]");
   if (k < 1 || k > kMaxPlaces) return fail(MGG_EINVAL, "k must be in [1, 32]");
   if (G < 1 || G > kMaxExperts) return fail(MGG_EINVAL, "G must be in [1, 4096]");
   const int unit = wt == MGG_WEIGHT_BF16 ? 8 : 128;
   if (H < 1 || H > kMaxWidth || H % unit || I < 1 || I > kMaxWidth || I % unit)
-    return fail(MGG_EINVAL, "H and I must be in [1, 2^17] and multiples of 8 (BF16) or 128");
+    return fail(MGG_EINVAL, "H and I must be in [1, 2^16] and multiples of 8 (BF16) or 128");
   const bool scaled = wt != MGG_WEIGHT_BF16;
   if (scaled) {
     if (sf != MGG_SF_F32 && sf != MGG_SF_UE8M0) return fail(MGG_EINVAL, "unknown scale format");
@@ -381,8 +467,7 @@ mgg_status moe_few_tokens(mgg_weight wt, int T, int k, int G, int H, int I, cons
   a.w13 = reinterpret_cast<const uint8_t*>(W13), a.w2 = reinterpret_cast<const uint8_t*>(W2);
   a.s13 = S13, a.s2 = S2;
   a.slot_meta = reinterpret_cast<int2*>(base + ws.meta);
-  a.slot_rows = reinterpret_cast<int32_t*>(base + ws.rows);
-  a.place_weight = reinterpret_cast<float*>(base + ws.weight);
+  a.slot_rows = reinterpret_cast<int2*>(base + ws.rows);
   a.h = reinterpret_cast<uint16_t*>(base + ws.h);
   a.h_low = reinterpret_cast<uint16_t*>(base + ws.h_low);
   a.out_dt = out_dt, a.residual = residual, a.ld_res = ld_res, a.out = out;

@@ -536,13 +536,17 @@ mgg_status run_tiles(const TileArgs& a, hipStream_t stream) {
 
 // The tile forms of a product, and what they are chosen by: how long one tile takes a CU that has
 // it alone (time for 2^20 multiply-adds, and for starting and storing a tile).
+//   large   256 x 256 by eight waves of 64 x 128: 1250 TFLOP/s in bfloat16 (8192 x 4096 x 4096), 144
+//           in float32 (4096 x 4096 x 4096)
+//   small   128 x 128 by eight waves of 32 x 64: 910 and 137
+//   narrow  128 x 64 by four waves of 32 x 64, float32: 118
 enum FormName { kLarge, kSmall, kNarrow };
 struct FormCost {
   int bm, bn;
   double us_per_m, us_fixed;
 };
-constexpr FormCost kBf16Forms[] = {{256, 256, 0.43, 6.0}, {128, 128, 0.57, 4.0}};
-constexpr FormCost kF32Forms[] = {{128, 128, 3.5, 4.0}, {128, 64, 3.6, 3.0}};
+constexpr FormCost kBf16Forms[] = {{256, 256, 0.43, 6.0}, {128, 128, 0.59, 4.0}};
+constexpr FormCost kF32Forms[] = {{256, 256, 3.73, 8.0}, {128, 128, 3.92, 5.0}, {128, 64, 4.55, 4.0}};
 
 struct Product {
   FormName form;
@@ -558,11 +562,11 @@ Product plan_product(bool f32, bool pairs, int64_t rows, int cols, int K) {
   Product best{};
   double best_us = 0;
   // a narrow tile has no room for blocks of gate and of up columns
-  for (int f = 0; f < (f32 && pairs ? 1 : 2); ++f) {
+  for (int f = 0; f < (f32 && !pairs ? 3 : 2); ++f) {
     const FormCost& c = f32 ? kF32Forms[f] : kBf16Forms[f];
     const int64_t m = (rows + c.bm - 1) / c.bm, n = cdiv(cols, c.bn);
     Product p{};
-    p.form = f32 ? (f ? kNarrow : kSmall) : (f ? kSmall : kLarge);
+    p.form = (FormName)f;
     p.counted = m * n < INT32_MAX / 64;
     const int slice = f32 ? 32 : 64, slices = std::max(1, cdiv(K, slice));
     const int64_t tiles = m * n;
@@ -598,16 +602,15 @@ mgg_status run_product(const Product& p, TileArgs a, hipStream_t stream) {
   a.deal = p.deal;
   // forms: waves along m and n, 32 x 32 blocks of a wave, stages, bytes of a slice, steps that
   // its copies are dealt to
-  if constexpr (!F32) {
-    if (p.form == kLarge)
-      return run_tiles<TileForm<false, TURN_X, TURN_W, PAIRS, 4, 2, 2, 4, 2, 128, 3>>(a, stream);
-  } else {
-    if constexpr (!PAIRS) {
-      if (p.form == kNarrow)
-        return run_tiles<TileForm<true, TURN_X, TURN_W, false, 4, 1, 1, 2, 2, 128, 2>>(a, stream);
-    }
-  }
-  return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 1, 1, 4, 2, 128, 2>>(a, stream);
+  if (p.form == kLarge)
+    return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 2, 2, 4, 2, 128, 3>>(a, stream);
+  if constexpr (F32 && !PAIRS)
+    if (p.form == kNarrow)
+      return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 1, 1, 2, 2, 128, 2>>(a, stream);
+  if constexpr (PAIRS)  // gate and up columns of a pair of blocks in one wave
+    return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 1, 1, 4, 2, 128, 2>>(a, stream);
+  else
+    return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 2, 1, 2, 3, 128, 2>>(a, stream);
 }
 
 // ---------------------------------------------------------------------------- few rows
@@ -630,22 +633,20 @@ __global__ __launch_bounds__(kRowThreads) void linear_rows(RowArgs a) {
   __shared__ __align__(16) float s_part[kRowWaves * RT * 16 * kPartLd];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * COLS;
-  StreamRows<RT> rows;
   const int n = min(n0 + (PAIRS ? r & 7 : r), a.e.C - 1) + (PAIRS && r >= 8 ? a.e.C : 0);
-  rows.w = a.w + n * a.ldw + q * F::RUN_BYTES;
-  rows.scale = nullptr;
-  rows.scale_step = 0;
+  const uint8_t* x[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int m = 16 * t + r;
-    rows.x[t] = m < a.M ? a.x + m * a.ldx + q * F::X_BYTES : nullptr;
+    x[t] = m < a.M ? a.x + m * a.ldx + q * F::X_BYTES : nullptr;
   }
   v4f acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = v4f{0.f, 0.f, 0.f, 0.f};
   const int blocks = cdiv(a.K, F::BLOCK);
-  stream_rows<W, kNoScales, kPerBlock, RT, false>(
-      rows, blocks * wave / kRowWaves, blocks * (wave + 1) / kRowWaves, a.K, acc);
+  stream_rows<W, RT, RT == 1 ? 6 : RT == 2 ? 4 : 2>(
+      a.w + n * a.ldw + q * F::RUN_BYTES, x, blocks * wave / kRowWaves,
+      blocks * (wave + 1) / kRowWaves, a.K, acc);
 #pragma unroll
   for (int t = 0; t < RT; ++t)
     *reinterpret_cast<v4f*>(s_part + ((wave * RT + t) * 16 + r) * kPartLd + 4 * q) = acc[t];
@@ -794,8 +795,10 @@ __global__ __launch_bounds__(64 * kSumWaves) void linear_bias_sum(const float* s
   __shared__ float s_sum[kSumWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = blockIdx.x * 64 + lane;
   float v = 0.f;
-  if (col < N)
+  if (col < N) {
+#pragma unroll 8
     for (int s = wave; s < strips; s += kSumWaves) v += sums[(int64_t)s * N + col];
+  }
   s_sum[wave][lane] = v;
   __syncthreads();
   if (wave == 0 && col < N) {

@@ -164,17 +164,25 @@ struct FragReader {
   }
 };
 
-template <bool F32>
-__device__ __forceinline__ v16f multiply(const Frag& w, const Frag& x, v16f acc) {
+// acc[j] += w[j] x^T over a step. Float32 takes four instructions a block; those of one block depend
+// on each other, so they alternate between the blocks.
+template <bool F32, int RJ>
+__device__ __forceinline__ void multiply(const Frag (&w)[RJ], const Frag& x, v16f (&acc)[RJ]) {
   if constexpr (F32) {
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w.x), __uint_as_float(x.x), acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w.y), __uint_as_float(x.y), acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w.z), __uint_as_float(x.z), acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(w.w), __uint_as_float(x.w), acc, 0, 0, 0);
-    return acc;
+    const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int j = 0; j < RJ; ++j) {
+        const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(ws[e]), __uint_as_float(xs[e]),
+                                                      acc[j], 0, 0, 0);
+      }
   } else {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, w),
-                                                   __builtin_bit_cast(v8bf, x), acc, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < RJ; ++j)
+      acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+          __builtin_bit_cast(v8bf, w[j]), __builtin_bit_cast(v8bf, x), acc[j], 0, 0, 0);
   }
 }
 
@@ -323,9 +331,7 @@ __device__ __forceinline__ void tile_stream(const Side& x, const Side& w, int64_
         }
 #pragma unroll
         for (int i = 0; i < T::RI; ++i) {
-#pragma unroll
-          for (int j = 0; j < T::RJ; ++j)
-            acc[i][j] = multiply<T::F32>(now.w[j], now.x[i], acc[i][j]);
+          multiply<T::F32>(now.w, now.x[i], acc[i]);
 #pragma unroll
           for (int n = 0; n < READS; ++n)
             if (n * T::RI / READS == i) read(next, n, last ? then : stage, last ? 0 : step + 1);

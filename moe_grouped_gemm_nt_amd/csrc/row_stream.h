@@ -63,81 +63,84 @@ __device__ __forceinline__ uint4 load16_part(const void* p, int bytes) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A lane's view of its operands, at K = 0 of its own run.
-template <int RT>
-struct StreamRows {
-  const uint8_t* w;             // its weight row
-  const void* scale;            // FP8: of its result rows; FP4: of its weight row
-  int64_t scale_step;           // elements from one block of 128 K to the next
-  const uint8_t* x[RT];         // its token rows; null: no row, zeros
-  const uint8_t* x_low[RT];     // the low halves of token rows held as two bfloat16
-};
-
-// One block of K in registers.
-template <WeightForm W, int RT, bool LOW>
-struct StreamBlock {
+// One block of K in registers: a lane's weights and the scales that go with them, and its runs of
+// token rows.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
+struct WeightBlock {
+  static constexpr int SCALES = W == kFp8Weights && SF == kF32Scales && SPAN == kPerChannel ? 4 : 1;
   uint4 w[Form<W>::LOADS];
-  float scale[4];
-  uint32_t scale_bits;
+  uint32_t scale[SCALES];  // as stored; the bytes of four rows in one word
+};
+template <WeightForm W, int RT, bool LOW>
+struct TokenBlock {
   uint4 x[RT][Form<W>::X_LOADS];
   uint4 x_low[LOW ? RT : 1][Form<W>::X_LOADS];
 };
 
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT, bool LOW>
-__device__ __forceinline__ void load_block(StreamBlock<W, RT, LOW>& b, const StreamRows<RT>& rows,
-                                           int block, int K) {
+// FP8 and FP4 rows are whole blocks of K; the others may end inside one.
+template <WeightForm W>
+struct Tail {
+  static constexpr bool POSSIBLE = W == kBf16Weights || W == kF32Weights;
+  static constexpr int ELEM = W == kF32Weights ? 4 : 2;
+  // whether block `block` is whole, and else how many bytes of the lane's run exist
+  static __device__ __forceinline__ bool whole(int block, int K) {
+    return !POSSIBLE || (block + 1) * Form<W>::BLOCK <= K;
+  }
+  static __device__ __forceinline__ int left(int block, int K) {
+    const int q = (threadIdx.x >> 4) & 3;
+    return (K - block * Form<W>::BLOCK - q * Form<W>::RUN) * ELEM;
+  }
+};
+
+// `w`, `scale`: the lane's weight row at K = 0 of its own run, and its scales there.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
+__device__ __forceinline__ void load_weights(WeightBlock<W, SF, SPAN>& b, const uint8_t* w,
+                                             const void* scale, int64_t scale_step, int block,
+                                             int K) {
   using F = Form<W>;
-  const int q = (threadIdx.x >> 4) & 3;
-  const int64_t w_at = (int64_t)block * (4 * F::RUN_BYTES), x_at = (int64_t)block * (4 * F::X_BYTES);
-  // FP8 and FP4 rows are whole blocks; the others may end inside one
-  constexpr bool TAIL = W == kBf16Weights || W == kF32Weights;
-  constexpr int ELEM = W == kF32Weights ? 4 : 2;
-  if (!TAIL || (block + 1) * F::BLOCK <= K) {
+  w += (int64_t)block * (4 * F::RUN_BYTES);
+  if (Tail<W>::whole(block, K)) {
 #pragma unroll
-    for (int i = 0; i < F::LOADS; ++i) b.w[i] = load16(rows.w + w_at + 16 * i);
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-      for (int i = 0; i < F::X_LOADS; ++i) {
-        b.x[t][i] = make_uint4(0, 0, 0, 0);
-        if (rows.x[t]) b.x[t][i] = load16(rows.x[t] + x_at + 16 * i);
-        if constexpr (LOW) {
-          b.x_low[t][i] = make_uint4(0, 0, 0, 0);
-          if (rows.x[t]) b.x_low[t][i] = load16(rows.x_low[t] + x_at + 16 * i);
-        }
-      }
+    for (int i = 0; i < F::LOADS; ++i) b.w[i] = load16(w + 16 * i);
   } else {
-    const int left = (K - block * F::BLOCK - q * F::RUN) * ELEM;  // bytes of its run that exist
+    const int left = Tail<W>::left(block, K);
 #pragma unroll
     for (int i = 0; i < F::LOADS; ++i)
-      b.w[i] = load16_part<ELEM>(rows.w + w_at + 16 * i, left - 16 * i);
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-#pragma unroll
-      for (int i = 0; i < F::X_LOADS; ++i) {
-        b.x[t][i] = make_uint4(0, 0, 0, 0);
-        if (rows.x[t]) b.x[t][i] = load16_part<ELEM>(rows.x[t] + x_at + 16 * i, left - 16 * i);
-        if constexpr (LOW) {
-          b.x_low[t][i] = make_uint4(0, 0, 0, 0);
-          if (rows.x[t])
-            b.x_low[t][i] = load16_part<ELEM>(rows.x_low[t] + x_at + 16 * i, left - 16 * i);
-        }
-      }
+      b.w[i] = load16_part<Tail<W>::ELEM>(w + 16 * i, left - 16 * i);
   }
-  if constexpr (W == kFp4Weights) {
-    b.scale_bits = reinterpret_cast<const uint8_t*>(rows.scale)[block * rows.scale_step];
-  } else if constexpr (W == kFp8Weights) {
-    const int64_t at = block * rows.scale_step;
-    if constexpr (SF == kF32Scales) {
-      const float* s = reinterpret_cast<const float*>(rows.scale) + at;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b.scale[i] = s[SPAN == kPerChannel ? i : 0];
-    } else {
-      const uint8_t* s = reinterpret_cast<const uint8_t*>(rows.scale) + at;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) b.scale[i] = byte_scale(s[SPAN == kPerChannel ? i : 0]);
-    }
+  if constexpr (W == kFp8Weights || W == kFp4Weights) {
+    constexpr int BYTES = SF == kF32Scales ? 4 : 1;
+    const uint8_t* s = reinterpret_cast<const uint8_t*>(scale) + block * scale_step * BYTES;
+    b.scale[0] = 0;
+    __builtin_memcpy(b.scale, s, W == kFp8Weights && SPAN == kPerChannel ? 4 * BYTES : BYTES);
   }
+}
+
+// A run of a token row at block `block`; a null row is zeros.
+template <WeightForm W>
+__device__ __forceinline__ void load_tokens(uint4 (&x)[Form<W>::X_LOADS], const uint8_t* row,
+                                            int block, int K) {
+  using F = Form<W>;
+#pragma unroll
+  for (int i = 0; i < F::X_LOADS; ++i) x[i] = make_uint4(0, 0, 0, 0);
+  if (!row) return;
+  row += (int64_t)block * (4 * F::X_BYTES);
+  if (Tail<W>::whole(block, K)) {
+#pragma unroll
+    for (int i = 0; i < F::X_LOADS; ++i) x[i] = load16(row + 16 * i);
+  } else {
+    const int left = Tail<W>::left(block, K);
+#pragma unroll
+    for (int i = 0; i < F::X_LOADS; ++i)
+      x[i] = load16_part<Tail<W>::ELEM>(row + 16 * i, left - 16 * i);
+  }
+}
+
+// Scale of the lane's i-th result row (FP8).
+template <ScaleForm SF, ScaleSpan SPAN, class Block>
+__device__ __forceinline__ float scale_of(const Block& b, int i) {
+  if constexpr (SF == kF32Scales) return __uint_as_float(b.scale[SPAN == kPerChannel ? i : 0]);
+  return byte_scale(b.scale[0] >> (SPAN == kPerChannel ? 8 * i : 0) & 255);
 }
 
 __device__ __forceinline__ v8bf as_bf16(const uint4& v) { return __builtin_bit_cast(v8bf, v); }
@@ -162,50 +165,61 @@ __device__ __forceinline__ v8bf from_e2m1(uint32_t a, float scale) {
   return as_bf16(v);
 }
 
-// acc += the block's products. FP8 scales multiply each block's float32 sum; FP4 scales, powers
-// of two, go into the conversion.
-template <WeightForm W, int RT, bool LOW>
-__device__ __forceinline__ void multiply_block(const StreamBlock<W, RT, LOW>& b, v4f (&acc)[RT]) {
+// A block's weights as the first operands of its matrix instructions (8- and 4-bit forms: exactly;
+// FP4 scales, powers of two, go into the conversion).
+template <WeightForm W, class Block>
+__device__ __forceinline__ void operands_of(const Block& b, v8bf (&w)[Form<W>::X_LOADS]) {
+  using F = Form<W>;
+  if constexpr (W == kBf16Weights) {
+#pragma unroll
+    for (int i = 0; i < F::X_LOADS; ++i) w[i] = as_bf16(b.w[i]);
+  } else if constexpr (W == kFp8Weights) {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(b.w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = from_e4m3(c[2 * i], c[2 * i + 1]);
+  } else {
+    const uint32_t* c = reinterpret_cast<const uint32_t*>(b.w);
+    // 255 (NaN) and 0 (2^-127) go through the exponent field as they are
+    const float scale = __uint_as_float(b.scale[0] << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = from_e2m1(c[i], scale);
+  }
+}
+
+// acc += the block's products. FP8 scales multiply each block's float32 sum. `x(t, i)` and
+// `x_low(t, i)` are the i-th 16 bytes of the lane's run of its t-th token row.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT, bool LOW, class Block, class X,
+          class XLow>
+__device__ __forceinline__ void multiply_block(const Block& b, v4f (&acc)[RT], X x, XLow x_low) {
   using F = Form<W>;
   if constexpr (W == kF32Weights) {
     float w[8];
     __builtin_memcpy(w, b.w, 32);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      float x[8];
-      __builtin_memcpy(x, b.x[t], 32);
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i], x[i], acc[t], 0, 0, 0);
-    }
+      for (int h = 0; h < 2; ++h) {
+        const v4f v = __builtin_bit_cast(v4f, x(t, h));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[4 * h + i], v[i], acc[t], 0, 0, 0);
+      }
   } else {
     v8bf w[F::X_LOADS];
-    if constexpr (W == kBf16Weights) {
-#pragma unroll
-      for (int i = 0; i < F::X_LOADS; ++i) w[i] = as_bf16(b.w[i]);
-    } else if constexpr (W == kFp8Weights) {
-      const uint32_t* c = reinterpret_cast<const uint32_t*>(b.w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = from_e4m3(c[2 * i], c[2 * i + 1]);
-    } else {
-      const uint32_t* c = reinterpret_cast<const uint32_t*>(b.w);
-      // 255 (NaN) and 0 (2^-127) go through the exponent field as they are
-      const float scale = __uint_as_float(b.scale_bits << 23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = from_e2m1(c[i], scale);
-    }
+    operands_of<W>(b, w);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       v4f sum = W == kFp8Weights ? v4f{0.f, 0.f, 0.f, 0.f} : acc[t];
 #pragma unroll
       for (int i = 0; i < F::X_LOADS; ++i) {
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(b.x[t][i]), sum, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(x(t, i)), sum, 0, 0, 0);
         if constexpr (LOW)
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(b.x_low[t][i]), sum, 0, 0, 0);
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(x_low(t, i)), sum, 0, 0, 0);
       }
       if constexpr (W == kFp8Weights) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[t][e] = fmaf(sum[e], b.scale[e], acc[t][e]);
+        for (int e = 0; e < 4; ++e)
+          acc[t][e] = fmaf(sum[e], scale_of<SF, SPAN>(b, e), acc[t][e]);
       } else {
         acc[t] = sum;
       }
@@ -213,15 +227,30 @@ __device__ __forceinline__ void multiply_block(const StreamBlock<W, RT, LOW>& b,
   }
 }
 
-// acc += products over the blocks [from, to) of K elements.
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT, bool LOW>
-__device__ __forceinline__ void stream_rows(const StreamRows<RT>& rows, int from, int to, int K,
-                                            v4f (&acc)[RT]) {
-  for (int b = from; b < to; ++b) {
-    StreamBlock<W, RT, LOW> block;
-    load_block<W, SF, SPAN>(block, rows, b, K);
-    multiply_block<W, RT, LOW>(block, acc);
-  }
+// acc += products over the blocks [from, to) of K elements, token rows from memory. AHEAD blocks
+// are on their way at a time: loads return in the order in which they were issued, so a block's
+// token rows are asked for together with its weights.
+template <WeightForm W, int RT, int AHEAD>
+__device__ __forceinline__ void stream_rows(const uint8_t* w, const uint8_t* const (&x)[RT],
+                                            int from, int to, int K, v4f (&acc)[RT]) {
+  WeightBlock<W, kNoScales, kPerBlock> weights[AHEAD];
+  TokenBlock<W, RT, false> tokens[AHEAD];
+  auto load = [&](int i, int b) {
+    load_weights<W, kNoScales, kPerBlock>(weights[i], w, nullptr, 0, b, K);
+#pragma unroll
+    for (int t = 0; t < RT; ++t) load_tokens<W>(tokens[i].x[t], x[t], b, K);
+  };
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (from + i < to) load(i, from + i);
+  for (int b = from; b < to; b += AHEAD)
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (b + i < to) {
+        auto x_of = [&](int t, int j) { return tokens[i].x[t][j]; };
+        multiply_block<W, kNoScales, kPerBlock, RT, false>(weights[i], acc, x_of, x_of);
+        if (b + i + AHEAD < to) load(i, b + i + AHEAD);
+      }
 }
 
 }  // namespace mgg_layer

@@ -61,7 +61,7 @@ def _scales(s, G, N, K, code, gran, like, name):
 
 def moe_few_tokens(x, ids, weights, w13, w2, s13=None, s2=None, sfb_gran=None, residual=None,
                    out=None, out_dtype=None, workspace=None):
-    """A whole MoE layer for few tokens (at most 256):
+    """A whole MoE layer for few tokens (at most 128):
         out[t] = residual[t] + sum_j weights[t, j] * w2[e] (silu(g) * u),  [g; u] = w13[e] x[t],
     e = ids[t, j], ids outside [0, G) skipped. x bf16 [T, H]; ids int32 and weights float32
     [T, k] (route_topk's); w13 [G, 2I, H] (gate rows, then up rows) and w2 [G, H, I] in bf16, FP8

@@ -47,10 +47,11 @@ def expert_weights(codes, scales, gran, fmt):
     return v * np.repeat(s, 128, 2)
 
 
-def moe_few_tokens(x, ids, weights, w13, w2, residual=None, roundings=None):
+def moe_few_tokens(x, ids, weights, w13, w2, residual=None, roundings=None, held=2.0 ** -17):
     """out [T, H]; with `roundings` (u: relative size of a float32 rounding) also a bound on what
     float32 sums may be off by, counting one rounding for each term of a sum, the gated unit's
-    own, and the 2^-17 relative error of a value held as two bfloat16."""
+    own, and `held`: the relative error of silu(g) u between the products (2^-17 as two bfloat16,
+    2^-8 as one)."""
     T, H = x.shape
     G, I = w13.shape[0], w13.shape[1] // 2
     out = np.zeros((T, H)) if residual is None else residual.copy()
@@ -69,7 +70,7 @@ def moe_few_tokens(x, ids, weights, w13, w2, residual=None, roundings=None):
             if roundings:
                 dz = (H + 8) * u * zs
                 dh = 1.1 * dz[:I] * np.abs(up) + np.abs(silu(g)) * dz[I:] \
-                    + ((16 + 2 * np.abs(g)) * u + 2.0 ** -17) * np.abs(h)
+                    + ((16 + 2 * np.abs(g)) * u + held) * np.abs(h)
                 err[t] += abs(weights[t, j]) * (np.abs(w2[e]) @ dh + (I + 8) * u * ys)
                 size[t] += np.abs(weights[t, j]) * ys
     return (out, err + (ids.shape[1] + 12) * u * size) if roundings else out

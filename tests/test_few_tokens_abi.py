@@ -38,10 +38,10 @@ def call(lib, wt=1, T=4, k=2, G=8, H=256, I=128, x=P, ldx=256, ids=P, w=P, w13=P
 @pytest.mark.parametrize("kw,code,text", [
     (dict(wt=3), EINVAL, "weight type"), (dict(wt=-1), EINVAL, "weight type"),
     (dict(out_dt=2), EINVAL, "element type"), (dict(T=-1), EINVAL, "T must"),
-    (dict(T=257), EINVAL, "T must"), (dict(k=0), EINVAL, "k must"), (dict(k=33), EINVAL, "k must"),
+    (dict(T=129), EINVAL, "T must"), (dict(k=0), EINVAL, "k must"), (dict(k=33), EINVAL, "k must"),
     (dict(G=0), EINVAL, "G must"), (dict(G=4097), EINVAL, "G must"),
     (dict(H=0), EINVAL, "H and I"), (dict(H=192), EINVAL, "H and I"),
-    (dict(I=64), EINVAL, "H and I"), (dict(I=1 << 18), EINVAL, "H and I"),
+    (dict(I=64), EINVAL, "H and I"), (dict(I=(1 << 16) + 128), EINVAL, "H and I"),
     (dict(wt=0, s13=NUL, s2=NUL, H=252), EINVAL, "H and I"),
     (dict(sf=2), EINVAL, "scale format"), (dict(gran=2), EUNSUPPORTED, "FP8 weights"),
     (dict(wt=2, gran=2), EUNSUPPORTED, "FP4 weights"),
@@ -70,7 +70,7 @@ def test_no_tokens_need_nothing(lib):
 def test_workspace_size(lib):
     size = lib.moe_few_tokens_workspace
     assert size(4, 2, 8, 128) >= 4 * 2 * 128 * 4
-    assert size(257, 2, 8, 128) == size(4, 33, 8, 128) == size(4, 2, 0, 128) == size(4, 2, 8, 0) == 0
+    assert size(129, 2, 8, 128) == size(4, 33, 8, 128) == size(4, 2, 0, 128) == size(4, 2, 8, 0) == 0
 
 
 def expect(pattern, exc=ValueError, **kw):
