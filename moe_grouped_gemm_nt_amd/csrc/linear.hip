@@ -276,18 +276,24 @@ __device__ __forceinline__ void store_blocks(const Lines& to, int row, int at,
   }
 }
 
-// v += the two blocks there.
+// Two such blocks on their way, as pieces of lines.
 template <bool F32>
-__device__ __forceinline__ void add_blocks(const Lines& from, int row, int at, float (&v)[2][16],
+__device__ __forceinline__ void load_blocks(const Lines& from, int row, int at, int lane,
+                                            uint4 (&p)[F32 ? 8 : 4]) {
+  const int r = row + (lane >> 3), c = (lane & 7) * 16;
+#pragma unroll
+  for (int k = 0; k < (F32 ? 8 : 4); ++k)
+    p[k] = __builtin_bit_cast(
+        uint4, mgg::load_b128(from.rsrc, from.offset(r + 8 * (k & 3),
+                                                     (at + 32 * (k >> 2)) * (F32 ? 4 : 2) + c)));
+}
+// v += those.
+template <bool F32>
+__device__ __forceinline__ void add_blocks(const uint4 (&lines)[F32 ? 8 : 4], float (&v)[2][16],
                                            const Turn& turn) {
-  const int r = row + (turn.lane >> 3), c = (turn.lane & 7) * 16;
-  uint4 p[4];
 #pragma unroll
   for (int b = 0; b < (F32 ? 2 : 1); ++b) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      p[k] = __builtin_bit_cast(
-          uint4, mgg::load_b128(from.rsrc, from.offset(r + 8 * k, (at + 32 * b) * (F32 ? 4 : 2) + c)));
+    uint4 p[4] = {lines[4 * b], lines[4 * b + 1], lines[4 * b + 2], lines[4 * b + 3]};
     turn.to_rows<F32>(p);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -355,6 +361,9 @@ __device__ __forceinline__ void finish_tile(const Emit& e, int64_t m0, int64_t n
     const Lines z_up(reinterpret_cast<uint8_t*>(e.z) + (int64_t)e.C * T::ELEM, T::F32, e.N, m0,
                      (int)n0, e.rows, e.C);
     const Lines res(e.residual, F32, e.ld_res, m0, (int)n0, e.rows, e.C);
+    // the residual of the next blocks is on its way while these are turned
+    uint4 ahead[F32 ? 8 : 4];
+    if (EPILOGUE && e.residual) load_blocks<F32>(res, row0, col0, lane, ahead);
 #pragma unroll
     for (int j = 0; j < T::RJ; j += 2 * P)
 #pragma unroll
@@ -389,7 +398,11 @@ __device__ __forceinline__ void finish_tile(const Emit& e, int64_t m0, int64_t n
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[0][b][r] = func_of(e.func, v[0][b][r]);
         }
-        if (EPILOGUE && e.residual) add_blocks<F32>(res, row, col, v[0], turn);
+        if (EPILOGUE && e.residual) {
+          add_blocks<F32>(ahead, v[0], turn);
+          if (i + 1 < T::RI) load_blocks<F32>(res, row + 32, col, lane, ahead);
+          else if (j + 2 * P < T::RJ) load_blocks<F32>(res, row0, col + 64, lane, ahead);
+        }
         store_blocks<F32>(out, row, col, v[0], turn);
         __builtin_amdgcn_sched_barrier(0);
       }

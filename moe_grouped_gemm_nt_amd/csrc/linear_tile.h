@@ -303,9 +303,6 @@ __device__ __forceinline__ void tile_stream(const Side& x, const Side& w, int64_
   begin_slice();
 #pragma unroll
   for (int i = 0; i < T::RI; ++i) copies(0, i);
-  Step now, next;
-#pragma unroll
-  for (int n = 0; n < READS; ++n) read(now, n, 0, 0);
   int stage = 0;
   TileAt t;
   for (int tile = 0; at(tile, t); ++tile) {
@@ -316,6 +313,10 @@ __device__ __forceinline__ void tile_stream(const Side& x, const Side& w, int64_
       for (int j = 0; j < T::RJ; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+    // read here and not at the end of the tile before: no registers of it while that is handed over
+    Step now, next;
+#pragma unroll
+    for (int n = 0; n < READS; ++n) read(now, n, stage, 0);
     const int slices = slices_of<T>(t.k_len);
     for (int s = 0; s < slices; ++s) {
       const int then = stage + 1 == T::S ? 0 : stage + 1;
