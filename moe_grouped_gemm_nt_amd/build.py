@@ -20,7 +20,8 @@ LIB_NAME = "libmoe_grouped_gemm_nt.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 # csrc/library.hip compiles csrc/grouped_gemm.hip
 SOURCES = ["csrc/library.hip", "csrc/quantize.hip", "csrc/route.hip", "csrc/block_norm.hip",
-           "csrc/newton_schulz.hip", "csrc/few_tokens.hip", "csrc/linear.hip"]
+           "csrc/newton_schulz.hip", "csrc/few_tokens.hip", "csrc/linear.hip",
+           "csrc/linear_forward.hip", "csrc/linear_backward.hip"]
 ARCH = "gfx950"
 
 
