@@ -153,7 +153,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
     WeightBlock<W, SF, SPAN> ring[kUpAhead];
 #pragma unroll
     for (int i = 0; i < kUpAhead; ++i)
-      if (from + i < to) load_weights<W, SF, SPAN>(ring[i], w, scale, scale_step, from + i, a.H);
+      if (from + i < to) load_weights<W, SF, SPAN, true>(ring[i], w, scale, scale_step, from + i, a.H);
     if (r0 > 0) __syncthreads();  // everyone is done with the rows and sums before
     const int pieces = (x_ld - 16) / 16;
     for (int row = 0; row < rows; row += 4) {
@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
           auto x = [&](int, int j) { return *reinterpret_cast<const uint4*>(xb + 16 * j); };
           multiply_block<W, SF, SPAN, 1, false>(ring[i], acc, x, x);
           if (b + i + kUpAhead < to)
-            load_weights<W, SF, SPAN>(ring[i], w, scale, scale_step, b + i + kUpAhead, a.H);
+            load_weights<W, SF, SPAN, true>(ring[i], w, scale, scale_step, b + i + kUpAhead, a.H);
         }
     *reinterpret_cast<v4f*>(s_part + (wave * 16 + r) * kPartLd + 4 * q) = acc[0];
     __syncthreads();
@@ -280,13 +280,13 @@ __global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) 
     const void* scale;
     int64_t step;
     set_scale<W, SF, SPAN>(a.s2, expert, a.H, a.I, ns, q, scale, step);
-    load_weights<W, SF, SPAN>(weights[i], w, scale, step, lb, a.I);
+    load_weights<W, SF, SPAN, true>(weights[i], w, scale, step, lb, a.I);
     const int place = r < count ? s_rows[row + r].x & 0xffff : -1;
     const int64_t at = (int64_t)place * a.I * 2 + q * F::X_BYTES;
-    load_tokens<W>(tokens[i].x[0], place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h) + at,
+    load_tokens<W, true>(tokens[i].x[0], place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h) + at,
                    lb, a.I);
     if constexpr (LOW)
-      load_tokens<W>(tokens[i].x_low[0],
+      load_tokens<W, true>(tokens[i].x_low[0],
                      place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h_low) + at, lb, a.I);
     if (++lb == blocks) lb = 0, ++lj;
   };
@@ -392,12 +392,12 @@ bool run_few(FewArgs a, hipStream_t stream) {
   const int half = (kLdsBytes / 2 - rest) / row, all = (kLdsBytes - rest) / row;
   a.x_rows = std::min(std::min(want, 16), half >= 4 || half >= want ? std::max(half, 1) : all);
   if (want > 8 && all >= 16) a.x_rows = 16;
-  // Tiles of a workgroup: as many as leave about three workgroups for each CU, and a block of K for
-  // each wave.
+  // Tiles of a workgroup: as many as leave a workgroup for each CU, and a block of K for each wave
+  // (32 tokens over six FP4 experts of 256 tiles: 58, 50.5 and 49 us with one, two and four).
   const int64_t tiles = (int64_t)cdiv(a.I, kUpColumns) * std::min(a.slots, a.places);
   const int blocks = cdiv(a.H, Form<W>::BLOCK);
-  const bool up = tiles >= 4 * 768 || blocks < 4 ? run_up<W, SF, SPAN, 4>(a, stream)
-                  : tiles >= 2 * 768 || blocks < 8 ? run_up<W, SF, SPAN, 2>(a, stream)
+  const bool up = tiles >= 4 * 300 || blocks < 4 ? run_up<W, SF, SPAN, 4>(a, stream)
+                  : tiles >= 2 * 300 || blocks < 8 ? run_up<W, SF, SPAN, 2>(a, stream)
                                                    : run_up<W, SF, SPAN, 1>(a, stream);
   const size_t lds = (size_t)kWaves * a.T * kDownColumns * 4 + a.places * sizeof(int2) +
                      kMaxJobs(a.slots, a.places) * 4;

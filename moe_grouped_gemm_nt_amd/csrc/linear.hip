@@ -21,13 +21,13 @@ constexpr int kFewRows = 64;  // up to here the weights stream past the rows
 //   large   256 x 256 by eight waves of 64 x 128: 1250 TFLOP/s in bfloat16 (8192 x 4096 x 4096), 144
 //           in float32 (4096 x 4096 x 4096)
 //   small   128 x 128 by eight waves of 32 x 64: 910 and 137
-//   narrow  128 x 64 by four waves of 32 x 64, float32: 118
+//   narrow  128 x 64 by eight waves of 32 x 32, float32: 125
 struct FormCost {
   int bm, bn;
   double us_per_m, us_fixed;
 };
 constexpr FormCost kBf16Forms[] = {{256, 256, 0.43, 6.0}, {128, 128, 0.59, 4.0}};
-constexpr FormCost kF32Forms[] = {{256, 256, 3.73, 8.0}, {128, 128, 3.92, 5.0}, {128, 64, 4.55, 4.0}};
+constexpr FormCost kF32Forms[] = {{256, 256, 3.73, 8.0}, {128, 128, 3.92, 5.0}, {128, 64, 4.3, 4.0}};
 
 // Tiles of [rows][cols] sums over K: the form, and how its tiles are dealt to the CUs, that cost
 // least. A last round of few tiles leaves CUs idle; its tiles are cut along K so that it fills

@@ -82,14 +82,16 @@ __device__ __forceinline__ uint32_t two_bf16(float a, float b) {  // one instruc
   return __builtin_bit_cast(uint32_t, v2{(__bf16)a, (__bf16)b});
 }
 
-// Stores two blocks of 32 columns (at columns `at` .. of the lines) of 32 rows (from `row` on).
-template <bool F32>
+// Stores NB blocks of 32 columns (at columns `at` .. of the lines) of 32 rows (from `row` on): two, or
+// one in float32.
+template <bool F32, int NB>
 __device__ __forceinline__ void store_blocks(const Lines& to, int row, int at,
-                                             const float (&v)[2][16], const Turn& turn) {
+                                             const float (&v)[NB][16], const Turn& turn) {
+  static_assert(F32 || NB == 2, "lines of 128 bytes");
   const int r = row + (turn.lane >> 3), c = (turn.lane & 7) * 16;
   uint4 p[4];
 #pragma unroll
-  for (int b = 0; b < (F32 ? 2 : 1); ++b) {
+  for (int b = 0; b < (F32 ? NB : 1); ++b) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if constexpr (F32) {
@@ -108,23 +110,23 @@ __device__ __forceinline__ void store_blocks(const Lines& to, int row, int at,
   }
 }
 
-// Two such blocks on their way, as pieces of lines.
-template <bool F32>
+// Such blocks on their way, as pieces of lines.
+template <bool F32, int NB>
 __device__ __forceinline__ void load_blocks(const Lines& from, int row, int at, int lane,
-                                            uint4 (&p)[F32 ? 8 : 4]) {
+                                            uint4 (&p)[F32 ? 4 * NB : 4]) {
   const int r = row + (lane >> 3), c = (lane & 7) * 16;
 #pragma unroll
-  for (int k = 0; k < (F32 ? 8 : 4); ++k)
+  for (int k = 0; k < (F32 ? 4 * NB : 4); ++k)
     p[k] = __builtin_bit_cast(
         uint4, mgg::load_b128(from.rsrc, from.offset(r + 8 * (k & 3),
                                                      (at + 32 * (k >> 2)) * (F32 ? 4 : 2) + c)));
 }
 // v += those.
-template <bool F32>
-__device__ __forceinline__ void add_blocks(const uint4 (&lines)[F32 ? 8 : 4], float (&v)[2][16],
-                                           const Turn& turn) {
+template <bool F32, int NB>
+__device__ __forceinline__ void add_blocks(const uint4 (&lines)[F32 ? 4 * NB : 4],
+                                           float (&v)[NB][16], const Turn& turn) {
 #pragma unroll
-  for (int b = 0; b < (F32 ? 2 : 1); ++b) {
+  for (int b = 0; b < (F32 ? NB : 1); ++b) {
     uint4 p[4] = {lines[4 * b], lines[4 * b + 1], lines[4 * b + 2], lines[4 * b + 3]};
     turn.to_rows<F32>(p);
 #pragma unroll
@@ -167,8 +169,8 @@ __device__ __forceinline__ void finish_tile(const Emit& e, int64_t m0, int64_t n
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   constexpr bool EPILOGUE = !T::TURN_W;  // gradients are stored as they are
   const int row0 = wave / T::WJ * 32 * T::RI, col0 = wave % T::WJ * (T::COLUMNS / T::WJ);
-  // two blocks of columns at a time; PAIRS: two of gate columns and their up columns
-  constexpr int P = T::PAIRS ? 2 : 1;
+  // two blocks of columns at a time, if a wave has two; PAIRS: of gate columns and their up columns
+  constexpr int P = T::PAIRS ? 2 : 1, NB = T::RJ >= 2 * P ? 2 : 1;
   if constexpr (OUT == kOutAny) {
 #pragma unroll
     for (int j = 0; j < T::RJ; j += P)
@@ -194,48 +196,48 @@ __device__ __forceinline__ void finish_tile(const Emit& e, int64_t m0, int64_t n
                      (int)n0, e.rows, e.C);
     const Lines res(e.residual, F32, e.ld_res, m0, (int)n0, e.rows, e.C);
     // the residual of the next blocks is on its way while these are turned
-    uint4 ahead[F32 ? 8 : 4];
-    if (EPILOGUE && e.residual) load_blocks<F32>(res, row0, col0, lane, ahead);
+    uint4 ahead[F32 ? 4 * NB : 4];
+    if (EPILOGUE && e.residual) load_blocks<F32, NB>(res, row0, col0, lane, ahead);
 #pragma unroll
-    for (int j = 0; j < T::RJ; j += 2 * P)
+    for (int j = 0; j < T::RJ; j += NB * P)
 #pragma unroll
       for (int i = 0; i < T::RI; ++i) {
         const int row = row0 + 32 * i, col = col0 + j / P * 32, n = (int)n0 + col;
-        float v[P][2][16];
+        float v[P][NB][16];
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[p][b][r] = acc[i][j + P * b + p][r];
         if (EPILOGUE && e.bias) {
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < NB; ++b)
               add_bias(e, p * e.C + n + 32 * b, e.C - n - 32 * b, lane, v[p][b]);
         }
         if (EPILOGUE && e.z) {
-          store_blocks<T::F32>(z, row, col, v[0], turn);
-          if constexpr (T::PAIRS) store_blocks<T::F32>(z_up, row, col, v[P - 1], turn);
+          store_blocks<T::F32, NB>(z, row, col, v[0], turn);
+          if constexpr (T::PAIRS) store_blocks<T::F32, NB>(z_up, row, col, v[P - 1], turn);
         }
         if constexpr (T::PAIRS) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[0][b][r] *= sigmoid(v[0][b][r]) * v[P - 1][b][r];
         } else if (EPILOGUE && e.func != MGG_FUNC_NONE) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b)
+          for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) v[0][b][r] = func_of(e.func, v[0][b][r]);
         }
         if (EPILOGUE && e.residual) {
-          add_blocks<F32>(ahead, v[0], turn);
-          if (i + 1 < T::RI) load_blocks<F32>(res, row + 32, col, lane, ahead);
-          else if (j + 2 * P < T::RJ) load_blocks<F32>(res, row0, col + 64, lane, ahead);
+          add_blocks<F32, NB>(ahead, v[0], turn);
+          if (i + 1 < T::RI) load_blocks<F32, NB>(res, row + 32, col, lane, ahead);
+          else if (j + NB * P < T::RJ) load_blocks<F32, NB>(res, row0, col + 32 * NB, lane, ahead);
         }
-        store_blocks<F32>(out, row, col, v[0], turn);
+        store_blocks<F32, NB>(out, row, col, v[0], turn);
         __builtin_amdgcn_sched_barrier(0);
       }
   }
@@ -363,7 +365,7 @@ mgg_status run_product(const Product& p, TileArgs a, hipStream_t stream) {
     return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 2, 2, 4, 2, 128, 3>>(a, stream);
   if constexpr (F32 && !PAIRS)
     if (p.form == kNarrow)
-      return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 1, 1, 2, 2, 128, 2>>(a, stream);
+      return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 2, 1, 1, 3, 128, 2>>(a, stream);
   if constexpr (PAIRS)  // gate and up columns of a pair of blocks in one wave
     return run_tiles<TileForm<F32, TURN_X, TURN_W, PAIRS, 4, 1, 1, 4, 2, 128, 2>>(a, stream);
   else

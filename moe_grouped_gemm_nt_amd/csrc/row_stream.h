@@ -92,8 +92,15 @@ struct Tail {
   }
 };
 
+// A piece of a run that may end in it, `left` bytes from its start. PIECES: rows are whole pieces.
+template <WeightForm W, bool PIECES>
+__device__ __forceinline__ uint4 load_end(const uint8_t* p, int left) {
+  if constexpr (PIECES) return left >= 16 ? load16(p) : make_uint4(0, 0, 0, 0);
+  else return load16_part<Tail<W>::ELEM>(p, left);
+}
+
 // `w`, `scale`: the lane's weight row at K = 0 of its own run, and its scales there.
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN>
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, bool PIECES>
 __device__ __forceinline__ void load_weights(WeightBlock<W, SF, SPAN>& b, const uint8_t* w,
                                              const void* scale, int64_t scale_step, int block,
                                              int K) {
@@ -106,7 +113,7 @@ __device__ __forceinline__ void load_weights(WeightBlock<W, SF, SPAN>& b, const 
     const int left = Tail<W>::left(block, K);
 #pragma unroll
     for (int i = 0; i < F::LOADS; ++i)
-      b.w[i] = load16_part<Tail<W>::ELEM>(w + 16 * i, left - 16 * i);
+      b.w[i] = load_end<W, PIECES>(w + 16 * i, left - 16 * i);
   }
   if constexpr (W == kFp8Weights || W == kFp4Weights) {
     constexpr int BYTES = SF == kF32Scales ? 4 : 1;
@@ -117,7 +124,7 @@ __device__ __forceinline__ void load_weights(WeightBlock<W, SF, SPAN>& b, const 
 }
 
 // A run of a token row at block `block`; a null row is zeros.
-template <WeightForm W>
+template <WeightForm W, bool PIECES>
 __device__ __forceinline__ void load_tokens(uint4 (&x)[Form<W>::X_LOADS], const uint8_t* row,
                                             int block, int K) {
   using F = Form<W>;
@@ -132,7 +139,7 @@ __device__ __forceinline__ void load_tokens(uint4 (&x)[Form<W>::X_LOADS], const 
     const int left = Tail<W>::left(block, K);
 #pragma unroll
     for (int i = 0; i < F::X_LOADS; ++i)
-      x[i] = load16_part<Tail<W>::ELEM>(row + 16 * i, left - 16 * i);
+      x[i] = load_end<W, PIECES>(row + 16 * i, left - 16 * i);
   }
 }
 
@@ -236,9 +243,9 @@ __device__ __forceinline__ void stream_rows(const uint8_t* w, const uint8_t* con
   WeightBlock<W, kNoScales, kPerBlock> weights[AHEAD];
   TokenBlock<W, RT, false> tokens[AHEAD];
   auto load = [&](int i, int b) {
-    load_weights<W, kNoScales, kPerBlock>(weights[i], w, nullptr, 0, b, K);
+    load_weights<W, kNoScales, kPerBlock, false>(weights[i], w, nullptr, 0, b, K);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) load_tokens<W>(tokens[i].x[t], x[t], b, K);
+    for (int t = 0; t < RT; ++t) load_tokens<W, false>(tokens[i].x[t], x[t], b, K);
   };
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i)
