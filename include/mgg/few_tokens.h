@@ -25,7 +25,7 @@ typedef enum { MGG_WEIGHT_BF16 = 0, MGG_WEIGHT_FP8 = 1, MGG_WEIGHT_FP4 = 2 } mgg
  * that names no expert gets its residual, or 0. An expert named twice by a token counts with the
  * sum of its weights. Weights are dequantized, activations are not quantized; sums are float32.
  * Between the products silu(g) * u is held as bfloat16 where the output is bfloat16, as between
- * the grouped products, and as two of them (16 significant bits) where it is float32.
+ * the grouped products, and as the sum of three (float32's 24 bits) where it is float32.
  *
  *   T, k, G     0 <= T <= 128; 1 <= k <= 32; 1 <= G <= 4096. The time goes with the experts
  *               that are named.

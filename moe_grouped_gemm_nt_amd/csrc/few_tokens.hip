@@ -36,7 +36,7 @@ struct FewArgs {
   int2* slot_meta;       // [slots]: tokens, expert
   int2* slot_rows;       // [slots][T]: for each token that names the expert its place (low 16 bits)
                          // and number, and what its output takes of the expert (float32 bits)
-  uint16_t *h, *h_low;   // [places][I]: silu(g) u as one bfloat16 or two
+  uint16_t* h;           // [planes][places][I]: silu(g) u as one bfloat16, or as the sum of three
   int x_rows;            // few_up: rows of x in LDS at a time
   mgg_act out_dt;
   const void* residual;
@@ -115,15 +115,14 @@ __host__ __device__ constexpr int x_row_bytes(int H) {
   return cdiv(H, Form<W>::BLOCK) * Form<W>::BLOCK * 2 + 16;
 }
 
-// AHEAD blocks of weights are on their way: 16 waves to a CU with 2 KB each (FP8).
-constexpr int kUpAhead = 4;
-
 // TILES: 8-column tiles of a workgroup, which shares K among kWaves / TILES waves for each. More
 // tiles mean fewer copies of x into LDS and longer streams, fewer workgroups.
 template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int TILES>
 __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
   using F = Form<W>;
   constexpr int PARTS = kWaves / TILES;
+  // blocks of weights on their way, within the 128 registers that leave 16 waves to a CU
+  constexpr int AHEAD = WeightBlock<W, SF, SPAN>::SCALES > 1 ? 3 : 4;
   extern __shared__ __align__(16) float s_few[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
   const int slot = blockIdx.y, tile = blockIdx.x * TILES + wave % TILES, part = wave / TILES;
@@ -150,9 +149,9 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
 
   for (int r0 = 0; r0 < count; r0 += a.x_rows) {
     const int rows = min(a.x_rows, count - r0);
-    WeightBlock<W, SF, SPAN> ring[kUpAhead];
+    WeightBlock<W, SF, SPAN> ring[AHEAD];
 #pragma unroll
-    for (int i = 0; i < kUpAhead; ++i)
+    for (int i = 0; i < AHEAD; ++i)
       if (from + i < to) load_weights<W, SF, SPAN, true>(ring[i], w, scale, scale_step, from + i, a.H);
     if (r0 > 0) __syncthreads();  // everyone is done with the rows and sums before
     const int pieces = (x_ld - 16) / 16;
@@ -176,15 +175,15 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
     v4f acc[1] = {v4f{0.f, 0.f, 0.f, 0.f}};
     // lanes without a row repeat the first one; nobody reads their results
     const uint8_t* xr = s_x + (r < rows ? r : 0) * x_ld + q * F::X_BYTES;
-    for (int b = from; b < to; b += kUpAhead)
+    for (int b = from; b < to; b += AHEAD)
 #pragma unroll
-      for (int i = 0; i < kUpAhead; ++i)
+      for (int i = 0; i < AHEAD; ++i)
         if (b + i < to) {
           const uint8_t* xb = xr + (b + i) * (4 * F::X_BYTES);
-          auto x = [&](int, int j) { return *reinterpret_cast<const uint4*>(xb + 16 * j); };
-          multiply_block<W, SF, SPAN, 1, false>(ring[i], acc, x, x);
-          if (b + i + kUpAhead < to)
-            load_weights<W, SF, SPAN, true>(ring[i], w, scale, scale_step, b + i + kUpAhead, a.H);
+          auto x = [&](int, int, int j) { return *reinterpret_cast<const uint4*>(xb + 16 * j); };
+          multiply_block<W, SF, SPAN, 1, 1>(ring[i], acc, x);
+          if (b + i + AHEAD < to)
+            load_weights<W, SF, SPAN, true>(ring[i], w, scale, scale_step, b + i + AHEAD, a.H);
         }
     *reinterpret_cast<v4f*>(s_part + (wave * 16 + r) * kPartLd + 4 * q) = acc[0];
     __syncthreads();
@@ -199,13 +198,16 @@ __global__ __launch_bounds__(kFewThreads, 4) void few_up(FewArgs a) {
         g += s[0];
         u += s[8];
       }
-      const float h = silu(g) * u;
-      const uint16_t hi = bf16_bits(h);
-      const int64_t at = (int64_t)list[r0 + row] * a.I + col;
-      a.h[at] = hi;
-      if (a.out_dt == MGG_ACT_F32) {
-        const float high = to_f32(bf16_t{hi});
-        a.h_low[at] = fabsf(high) < INFINITY ? bf16_bits(h - high) : 0;
+      // Bfloat16 outputs: as between the grouped products, h is rounded to their type. Float32
+      // outputs: three bfloat16 are the 24 bits of h (an infinite one stays alone).
+      float h = silu(g) * u;
+      uint16_t* to = a.h + (int64_t)list[r0 + row] * a.I + col;
+      const int64_t plane = (int64_t)a.places * a.I;
+      for (int p = 0; p < (a.out_dt == MGG_ACT_F32 ? 3 : 1); ++p) {
+        const uint16_t bits = bf16_bits(h);
+        to[p * plane] = bits;
+        const float held = to_f32(bf16_t{bits});
+        h = fabsf(held) < INFINITY ? h - held : 0.f;
       }
     }
   }
@@ -226,11 +228,10 @@ __device__ __forceinline__ uint32_t pack_job(int row, int count, int expert) {
 }
 constexpr int kMaxJobs(int slots, int places) { return slots + places / 16; }
 
-// LOW: h is two bfloat16.
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, bool LOW>
-__global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) {
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int PLANES>
+__global__ __launch_bounds__(kFewThreads, PLANES > 1 ? 2 : 4) void few_down(FewArgs a) {
   using F = Form<W>;
-  constexpr int AHEAD = LOW ? 3 : W == kBf16Weights ? 4 : 3;
+  constexpr int AHEAD = W == kBf16Weights ? 4 : PLANES > 1 ? 2 : 3;
   extern __shared__ __align__(16) float s_few[];
   __shared__ int2 s_total[kWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, q = lane >> 4;
@@ -270,7 +271,7 @@ __global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) 
   const int end = (int)((int64_t)units * (wave + 1) / kWaves);
   const int n = min(n0 + r, a.H - 1), ns = W == kFp4Weights ? n : min(n0 + 4 * q, a.H - 4);
   WeightBlock<W, SF, SPAN> weights[AHEAD];
-  TokenBlock<W, 1, LOW> tokens[AHEAD];
+  TokenBlock<W, 1, PLANES> tokens[AHEAD];
   // the unit to load next: block `lb` of job `lj`
   int lj = first / blocks, lb = first % blocks;
   auto load = [&](int i) {
@@ -283,11 +284,13 @@ __global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) 
     load_weights<W, SF, SPAN, true>(weights[i], w, scale, step, lb, a.I);
     const int place = r < count ? s_rows[row + r].x & 0xffff : -1;
     const int64_t at = (int64_t)place * a.I * 2 + q * F::X_BYTES;
-    load_tokens<W, true>(tokens[i].x[0], place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h) + at,
-                   lb, a.I);
-    if constexpr (LOW)
-      load_tokens<W, true>(tokens[i].x_low[0],
-                     place < 0 ? nullptr : reinterpret_cast<const uint8_t*>(a.h_low) + at, lb, a.I);
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p)
+      load_tokens<W, true>(tokens[i].x[p][0],
+                           place < 0 ? nullptr
+                                     : reinterpret_cast<const uint8_t*>(a.h) + at +
+                                           p * ((int64_t)a.places * a.I * 2),
+                           lb, a.I);
     if (++lb == blocks) lb = 0, ++lj;
   };
 #pragma unroll
@@ -299,9 +302,8 @@ __global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) 
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
       if (u + i < end) {
-        auto x = [&](int, int j) { return tokens[i].x[0][j]; };
-        auto x_low = [&](int, int j) { return tokens[i].x_low[0][j]; };
-        multiply_block<W, SF, SPAN, 1, LOW>(weights[i], acc, x, x_low);
+        auto x = [&](int p, int, int j) { return tokens[i].x[p][0][j]; };
+        multiply_block<W, SF, SPAN, 1, PLANES>(weights[i], acc, x);
         if (u + i + AHEAD < end) load(i);
         if (++block_at == blocks || u + i + 1 == end) {
           // a wave's tokens of one job are different ones
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(kFewThreads, LOW ? 2 : 4) void few_down(FewArgs a) 
 
 // Where the workspace's parts start.
 struct FewWorkspace {
-  size_t meta, rows, h, h_low, bytes;
+  size_t meta, rows, h, bytes;
   FewWorkspace(int T, int k, int G, int I) {
     const size_t places = (size_t)T * k, slots = std::min<size_t>(places, G);
     size_t at = 0;
@@ -352,8 +354,7 @@ struct FewWorkspace {
     };
     meta = take(slots * sizeof(int2));
     rows = take(slots * T * sizeof(int2));
-    h = take(places * I * 2);
-    h_low = take(places * I * 2);
+    h = take(3 * places * I * 2);
     bytes = at;
   }
 };
@@ -402,8 +403,8 @@ bool run_few(FewArgs a, hipStream_t stream) {
   const size_t lds = (size_t)kWaves * a.T * kDownColumns * 4 + a.places * sizeof(int2) +
                      kMaxJobs(a.slots, a.places) * 4;
   const dim3 grid(cdiv(a.H, kDownColumns));
-  return up && (a.out_dt == MGG_ACT_F32 ? launch_few(few_down<W, SF, SPAN, true>, grid, lds, a, stream)
-                                        : launch_few(few_down<W, SF, SPAN, false>, grid, lds, a, stream));
+  return up && (a.out_dt == MGG_ACT_F32 ? launch_few(few_down<W, SF, SPAN, 3>, grid, lds, a, stream)
+                                        : launch_few(few_down<W, SF, SPAN, 1>, grid, lds, a, stream));
 }
 
 }  // namespace
@@ -469,7 +470,6 @@ mgg_status moe_few_tokens(mgg_weight wt, int T, int k, int G, int H, int I, cons
   a.slot_meta = reinterpret_cast<int2*>(base + ws.meta);
   a.slot_rows = reinterpret_cast<int2*>(base + ws.rows);
   a.h = reinterpret_cast<uint16_t*>(base + ws.h);
-  a.h_low = reinterpret_cast<uint16_t*>(base + ws.h_low);
   a.out_dt = out_dt, a.residual = residual, a.ld_res = ld_res, a.out = out;
 
   bool ok;

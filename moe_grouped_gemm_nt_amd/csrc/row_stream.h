@@ -71,10 +71,10 @@ struct WeightBlock {
   uint4 w[Form<W>::LOADS];
   uint32_t scale[SCALES];  // as stored; the bytes of four rows in one word
 };
-template <WeightForm W, int RT, bool LOW>
+// A token row may be the sum of PLANES rows of bfloat16.
+template <WeightForm W, int RT, int PLANES>
 struct TokenBlock {
-  uint4 x[RT][Form<W>::X_LOADS];
-  uint4 x_low[LOW ? RT : 1][Form<W>::X_LOADS];
+  uint4 x[PLANES][RT][Form<W>::X_LOADS];
 };
 
 // FP8 and FP4 rows are whole blocks of K; the others may end inside one.
@@ -193,11 +193,10 @@ __device__ __forceinline__ void operands_of(const Block& b, v8bf (&w)[Form<W>::X
   }
 }
 
-// acc += the block's products. FP8 scales multiply each block's float32 sum. `x(t, i)` and
-// `x_low(t, i)` are the i-th 16 bytes of the lane's run of its t-th token row.
-template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT, bool LOW, class Block, class X,
-          class XLow>
-__device__ __forceinline__ void multiply_block(const Block& b, v4f (&acc)[RT], X x, XLow x_low) {
+// acc += the block's products. FP8 scales multiply each block's float32 sum. `x(p, t, i)` is the i-th
+// 16 bytes of the lane's run of plane p of its t-th token row.
+template <WeightForm W, ScaleForm SF, ScaleSpan SPAN, int RT, int PLANES, class Block, class X>
+__device__ __forceinline__ void multiply_block(const Block& b, v4f (&acc)[RT], X x) {
   using F = Form<W>;
   if constexpr (W == kF32Weights) {
     float w[8];
@@ -206,7 +205,7 @@ __device__ __forceinline__ void multiply_block(const Block& b, v4f (&acc)[RT], X
     for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const v4f v = __builtin_bit_cast(v4f, x(t, h));
+        const v4f v = __builtin_bit_cast(v4f, x(0, t, h));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[4 * h + i], v[i], acc[t], 0, 0, 0);
@@ -218,11 +217,10 @@ __device__ __forceinline__ void multiply_block(const Block& b, v4f (&acc)[RT], X
     for (int t = 0; t < RT; ++t) {
       v4f sum = W == kFp8Weights ? v4f{0.f, 0.f, 0.f, 0.f} : acc[t];
 #pragma unroll
-      for (int i = 0; i < F::X_LOADS; ++i) {
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(x(t, i)), sum, 0, 0, 0);
-        if constexpr (LOW)
-          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(x_low(t, i)), sum, 0, 0, 0);
-      }
+      for (int p = 0; p < PLANES; ++p)
+#pragma unroll
+        for (int i = 0; i < F::X_LOADS; ++i)
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i], as_bf16(x(p, t, i)), sum, 0, 0, 0);
       if constexpr (W == kFp8Weights) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -241,11 +239,11 @@ template <WeightForm W, int RT, int AHEAD>
 __device__ __forceinline__ void stream_rows(const uint8_t* w, const uint8_t* const (&x)[RT],
                                             int from, int to, int K, v4f (&acc)[RT]) {
   WeightBlock<W, kNoScales, kPerBlock> weights[AHEAD];
-  TokenBlock<W, RT, false> tokens[AHEAD];
+  TokenBlock<W, RT, 1> tokens[AHEAD];
   auto load = [&](int i, int b) {
     load_weights<W, kNoScales, kPerBlock, false>(weights[i], w, nullptr, 0, b, K);
 #pragma unroll
-    for (int t = 0; t < RT; ++t) load_tokens<W, false>(tokens[i].x[t], x[t], b, K);
+    for (int t = 0; t < RT; ++t) load_tokens<W, false>(tokens[i].x[0][t], x[t], b, K);
   };
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i)
@@ -254,8 +252,8 @@ __device__ __forceinline__ void stream_rows(const uint8_t* w, const uint8_t* con
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
       if (b + i < to) {
-        auto x_of = [&](int t, int j) { return tokens[i].x[t][j]; };
-        multiply_block<W, kNoScales, kPerBlock, RT, false>(weights[i], acc, x_of, x_of);
+        auto x_of = [&](int, int t, int j) { return tokens[i].x[0][t][j]; };
+        multiply_block<W, kNoScales, kPerBlock, RT, 1>(weights[i], acc, x_of);
         if (b + i + AHEAD < to) load(i, b + i + AHEAD);
       }
 }

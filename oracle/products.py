@@ -47,11 +47,11 @@ def expert_weights(codes, scales, gran, fmt):
     return v * np.repeat(s, 128, 2)
 
 
-def moe_few_tokens(x, ids, weights, w13, w2, residual=None, roundings=None, held=2.0 ** -17):
+def moe_few_tokens(x, ids, weights, w13, w2, residual=None, roundings=None, held=2.0 ** -24):
     """out [T, H]; with `roundings` (u: relative size of a float32 rounding) also a bound on what
     float32 sums may be off by, counting one rounding for each term of a sum, the gated unit's
-    own, and `held`: the relative error of silu(g) u between the products (2^-17 as two bfloat16,
-    2^-8 as one)."""
+    own, and `held`: the relative error of silu(g) u between the products (2^-8
+    as one bfloat16, 2^-24 as three)."""
     T, H = x.shape
     G, I = w13.shape[0], w13.shape[1] // 2
     out = np.zeros((T, H)) if residual is None else residual.copy()
