@@ -14,7 +14,7 @@ namespace {
 
 using namespace mgg_dense;
 
-constexpr int kFewRows = 64;  // up to here the weights stream past the rows
+constexpr int kFewRows = 64;  // up to here the weights stream past the rows (linear_rows)
 
 // The tile forms of a product, and what they are chosen by: how long one tile takes a CU that has
 // it alone (time for 2^20 multiply-adds, and for starting and storing a tile).
@@ -82,6 +82,9 @@ struct RowArgs {
 };
 
 // 16 weight rows (PAIRS: 8 gate rows and their 8 up rows) times all rows of x; the waves share K.
+// Bound by the weights' way from HBM, with more rows by that of x from L2, which every workgroup reads
+// whole. Measured in bfloat16: one row, 7168 x 2048: 29 MB in 7.9 us; 48 rows, 4096 x 4096 with SwiGLU
+// 16.7 us, where tiles cut along K take 20 (33 to 128 rows: 19 to 23 us).
 template <bool F32, bool PAIRS, int RT>
 __global__ __launch_bounds__(kRowThreads) void linear_rows(RowArgs a) {
   constexpr WeightForm W = F32 ? kF32Weights : kBf16Weights;
@@ -181,7 +184,7 @@ __device__ __forceinline__ float grad_of(mgg_func f, float z, float d) {
   }
 }
 
-// dz and its column sums: a workgroup takes a strip of rows of 512 columns of d_out, eight columns
+// dz and its column sums, bound by HBM (8192 x 4096 bfloat16: 201 MB in 53 us): a workgroup takes a strip of rows of 512 columns of d_out, eight columns
 // a lane, its four waves row by row in turn.
 constexpr int kGradColumns = 512, kGradWaves = 4;
 template <bool PAIRS>
