@@ -84,13 +84,13 @@ def moe_few_tokens(x, ids, weights, w13, w2, s13=None, s2=None, sfb_gran=None, r
         raise ValueError("weights must be float32 [T, k]")
     code = _weight(w13, w2, G, H, I)
     gran = sfb_gran or ("block32" if code == MGG_WEIGHT_FP4 else "block128")
+    allowed = ("block32",) if code == MGG_WEIGHT_FP4 else ("block128", "channel")
+    if gran not in allowed:
+        raise ValueError(f"weight-scale granularity {gran!r} does not fit these weights "
+                         f"(expected one of {list(allowed)})")
     if code == MGG_WEIGHT_BF16:
         _mgg._require(s13 is None and s2 is None, "bf16 weights take no scales")
     else:
-        allowed = ("block32",) if code == MGG_WEIGHT_FP4 else ("block128", "channel")
-        if gran not in allowed:
-            raise ValueError(f"weight-scale granularity {gran!r} does not fit these weights "
-                             f"(expected one of {list(allowed)})")
         _scales(s13, G, 2 * I, H, code, gran, s13, "s13")
         _scales(s2, G, H, I, code, gran, s13, "s2")
     out_dtype = out.dtype if out is not None else (out_dtype or torch.bfloat16)

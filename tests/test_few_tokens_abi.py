@@ -109,3 +109,10 @@ def test_binding_refuses():
     expect("s13 .* must be", s13=z(8, 2, 2).double())
     expect("does not fit", sfb_gran="block32")
     expect("no scales", w13=z(8, 256, 256, dtype=bf), w2=z(8, 256, 128, dtype=bf))
+
+
+@pytest.mark.parametrize("gran", ["block64", "block32"])
+def test_bf16_weights_refuse_an_unfit_granularity(gran):
+    bf = torch.bfloat16
+    expect("does not fit", w13=torch.zeros(8, 256, 256, dtype=bf), s13=None, s2=None,
+           w2=torch.zeros(8, 256, 128, dtype=bf), sfb_gran=gran)
